@@ -62,9 +62,13 @@ typedef enum {
     FLARE_ERR_WORKSPACE = 3,    /* workspace missing or smaller than required    */
     FLARE_ERR_CUDA = 4,         /* a CUDA runtime call or launch failed          */
     FLARE_ERR_TIMEOUT = 5,      /* a kernel gave up a bounded wait (device flag) */
-    FLARE_ERR_DEVICE_CHECK = 6  /* a device-side check of a FLARE_DEBUG build of
+    FLARE_ERR_DEVICE_CHECK = 6, /* a device-side check of a FLARE_DEBUG build of
                                    the library failed (device flag); the access
                                    it guarded was skipped                        */
+    FLARE_ERR_CACHE = 7         /* a token cache call met a page number outside the
+                                   pool, a length outside the page table or row
+                                   offsets out of range (device flag); what they
+                                   name was skipped                              */
 } flare_status_t;
 
 typedef enum { FLARE_F32 = 0, FLARE_BF16 = 1 } flare_dtype_t;
@@ -333,6 +337,127 @@ FLARE_API flare_status_t flare_encoder_fwd_noalloc(const flare_dims_t *dims, con
                                                    const int64_t *shard_offsets, int R, float *O_r,
                                                    float *L_r, float *Z, float *L, void *stream);
 
+/*
+ * ---- Paged 8-bit token cache ------------------------------------------------
+ * Keys and values of B sequences of any lengths, held as e4m3 codes in pages of
+ * `page` tokens. A page and head have one scale each for keys and for values:
+ * an element is its code times the scale. Everything the sequences' lengths
+ * decide is worked out on the device, so that a call can be captured once and
+ * replayed while they grow.
+ */
+typedef struct {
+    int B;                  /* sequences                                       */
+    int H;                  /* heads of the cache                              */
+    int Hq;                 /* query heads: a multiple of H (0: no queries);
+                               query head j reads cache head j / (Hq / H)      */
+    int D;                  /* head dimension: a multiple of 16, 16..128       */
+    int page;               /* tokens of a page: 16, 32, 64 or 128             */
+    int W;                  /* columns of the page table (>= 1)                */
+    int64_t P;              /* pages of the pool (>= 1)                        */
+    float scale;            /* score scale s; <= 0 selects s = D^-1/2          */
+    flare_dtype_t dtype;    /* element type of the tokens, queries and outputs */
+    flare_kernel_t kernel;  /* kernel family (FLARE_KERNEL_AUTO by default)    */
+} flare_cache_dims_t;
+
+typedef struct {
+    void *k, *v;                /* e4m3 codes [P, H, page, D], 16-byte aligned */
+    float *k_scale, *v_scale;   /* [P, H]; powers of two 2^-40 .. 2^60         */
+    const int32_t *page_table;  /* [B, W]: page of tokens w*page .. of sequence b */
+} flare_cache_t;
+
+/*
+ * New tokens enter the cache, keys (and queries) rotated by their positions.
+ * Sequence b holds seq_lens[b] tokens and gets n_b new ones, at positions
+ * seq_lens[b], seq_lens[b] + 1, ...; position p lies in slot p % page of page
+ * page_table[b, p / page].
+ *   K, V       dims->dtype [T, H, D]: the new tokens of all sequences, one
+ *              sequence after another; elements between two tokens are
+ *              k_stride, v_stride (0: H*D; a slice of a wider row is fine)
+ *   seq_lens   int32 [B], tokens held before the call (device)
+ *   cu_seqlens int32 [B+1] (device): sequence b's rows are
+ *              [cu_seqlens[b], cu_seqlens[b+1]) of the T; NULL: T/B rows each
+ *   Q, Q_out   dims->dtype [T, Hq, D] queries (elements between tokens
+ *              q_stride, 0: Hq*D) and where their rotation goes (dense; may
+ *              not overlap Q); both NULL: no queries
+ *   inv_freq   fp32 [rot/2] (device) or NULL (no rotation): channel pair j of
+ *              the first `rot` channels is turned by the angle
+ *              position * inv_freq[j]; pairs are (j, j + rot/2), or
+ *              (2j, 2j+1) where `interleaved`
+ *   seq_lens_out  int32 [B]: tokens held after the call (may not overlap
+ *              seq_lens), or NULL
+ * Scales: with A the largest magnitude of the new tokens of a page and head
+ * before the rotation, 2^(ceil(log2 A) - 8); where the page held tokens of the
+ * sequence already, the larger of that and its scale, and their codes are
+ * rounded anew if it grew. A magnitude beyond 448 * 2^60 is held as that. A
+ * token and head with a channel that is not finite is held as a NaN key and a
+ * zero value: it makes every row that sees it NaN, and no other.
+ * Slots behind the last new token keep what they hold. A page that a call
+ * writes belongs to one sequence of that call; pages that it only reads (full
+ * ones) may be shared. Tokens that the table has no room or no valid page for
+ * are dropped and the device status is set (FLARE_ERR_CACHE). No workspace.
+ */
+FLARE_API flare_status_t flare_cache_append(const flare_cache_dims_t *dims, const flare_cache_t *cache,
+                                            const void *K, const void *V, int64_t k_stride,
+                                            int64_t v_stride, int64_t T, const int32_t *seq_lens,
+                                            const int32_t *cu_seqlens, const void *Q,
+                                            int64_t q_stride, void *Q_out, const float *inv_freq,
+                                            int rot, int interleaved, int32_t *seq_lens_out,
+                                            void *stream);
+
+/* Workspace bytes of flare_cache_attn for T query rows (of
+ * flare_cache_encoder_fwd and flare_cache_fwd for T = B*M and dims->Hq =
+ * dims->H); (size_t)-1 when the sizes are invalid. */
+FLARE_API size_t flare_cache_workspace_bytes(const flare_cache_dims_t *dims, int64_t T);
+
+/*
+ * Attention of query rows over the cache. Row i of sequence b's n_b sees the
+ * seq_lens[b] tokens held (new ones among them); where `causal`, only those up
+ * to its own position seq_lens[b] - n_b + i. Per row and query head:
+ *   S_n = s <q, k_n>,  L = log sum_n exp(S_n),  O = sum_n exp(S_n - L) v_n;
+ * a row that sees no token gives O = 0 and L = -inf.
+ *   Q  dims->dtype [T, Hq, D] (elements between tokens q_stride, 0: Hq*D);
+ *   seq_lens, cu_seqlens: as for flare_cache_append, seq_lens after it;
+ *   O  dims->dtype [T, Hq, D];  L fp32 [T, Hq] or NULL.
+ * Rows of Q behind the last sequence are not read and theirs of O and L keep
+ * what they hold. A token on a page number outside the pool is not seen, and
+ * the device status is set. Softmax and sums are fp32; the kernels for bf16
+ * round the weights exp(S - max) to fp16 where they meet the values.
+ * workspace: flare_cache_workspace_bytes(dims, T) bytes, 256-byte aligned.
+ */
+FLARE_API flare_status_t flare_cache_attn(const flare_cache_dims_t *dims, const flare_cache_t *cache,
+                                          const void *Q, int64_t q_stride, int64_t T,
+                                          const int32_t *seq_lens, const int32_t *cu_seqlens,
+                                          int causal, void *O, float *L, void *workspace,
+                                          size_t workspace_bytes, void *stream);
+
+/*
+ * The FLARE encoder over a cached token set: flare_encoder_fwd with the keys
+ * and values of the cache, each batch element of its own length. dims->Hq is
+ * not read; M latent queries per head.
+ *   Q  dims->dtype [H,M,D] (q_batch_stride 0) or [B,H,M,D] (H*M*D);
+ *   Z  fp32 [B,H,M,D];  L fp32 [B,H,M].
+ */
+FLARE_API flare_status_t flare_cache_encoder_fwd(const flare_cache_dims_t *dims,
+                                                 const flare_cache_t *cache, int M, const void *Q,
+                                                 int64_t q_batch_stride, const int32_t *seq_lens,
+                                                 float *Z, float *L, void *workspace,
+                                                 size_t workspace_bytes, void *stream);
+
+/*
+ * FLARE mixer forward over a growing token set: the N new tokens of every
+ * sequence enter the cache (flare_cache_append without rotation), the latents
+ * gather Z from all the tokens held (flare_cache_encoder_fwd), and the new
+ * tokens decode against them (flare_decode_fwd).
+ *   Q as for flare_cache_encoder_fwd; K, V, Y dims->dtype [B,N,H,D];
+ *   seq_lens int32 [B] before, seq_lens_out int32 [B] after the call (given,
+ *   and not overlapping); Z, L as for flare_cache_encoder_fwd.
+ */
+FLARE_API flare_status_t flare_cache_fwd(const flare_cache_dims_t *dims, const flare_cache_t *cache,
+                                         int M, int N, const void *Q, int64_t q_batch_stride,
+                                         const void *K, const void *V, const int32_t *seq_lens,
+                                         int32_t *seq_lens_out, void *Y, float *Z, float *L,
+                                         void *workspace, size_t workspace_bytes, void *stream);
+
 /* Failure-path check of the bounded waits (no counterpart on the pages).
  * Launches, on `stream`, one small kernel whose only work is a wait on an
  * mbarrier that nothing arrives on; after limit_us microseconds (1..1000000)
@@ -348,9 +473,9 @@ FLARE_API flare_status_t flare_check_bounded_wait(unsigned limit_us, void *strea
 /* Synchronises `stream`, then reads and clears the device status word that
  * kernels set when they abandon a bounded wait (or, in a FLARE_DEBUG build,
  * when a device-side check of a tile's place or a workspace index fails; the
- * first error recorded wins): FLARE_OK, FLARE_ERR_TIMEOUT,
- * FLARE_ERR_DEVICE_CHECK, or FLARE_ERR_CUDA if the synchronisation itself
- * failed. */
+ * first error recorded wins), or when a token cache call met something out of
+ * range: FLARE_OK, FLARE_ERR_TIMEOUT, FLARE_ERR_DEVICE_CHECK, FLARE_ERR_CACHE,
+ * or FLARE_ERR_CUDA if the synchronisation itself failed. */
 FLARE_API flare_status_t flare_device_status(void *stream);
 
 /* Text of the calling thread's most recent error (empty if none). */

@@ -1,0 +1,291 @@
+// cache_api.cu -- C ABI of the paged 8-bit token cache (include/flare.h):
+// argument checks, workspace carve-up and launches.
+#include "cache_common.cuh"
+
+#include <cmath>
+#include <cstdarg>
+#include <cstdio>
+
+namespace flare {
+namespace {
+
+using namespace cache;
+
+flare_status_t fail(flare_status_t s, const char *fmt, ...) {
+    char buf[512];
+    va_list ap;
+    va_start(ap, fmt);
+    vsnprintf(buf, sizeof buf, fmt, ap);
+    va_end(ap);
+    return report_error(s, buf);
+}
+
+bool aligned(const void *p, size_t a) { return ((uintptr_t)p % a) == 0; }
+
+size_t elem_size(const flare_cache_dims_t *d) { return d->dtype == FLARE_BF16 ? 2 : 4; }
+
+flare_status_t check_dims(const flare_cache_dims_t *d) {
+    if (!d) return fail(FLARE_ERR_INVALID_ARG, "dims is NULL");
+    if (d->B < 0) return fail(FLARE_ERR_INVALID_ARG, "B must be >= 0");
+    if (d->H < 1 || d->H > 1024) return fail(FLARE_ERR_INVALID_ARG, "H=%d outside [1, 1024]", d->H);
+    if (d->Hq < 0 || d->Hq > 16384 || d->Hq % d->H)
+        return fail(FLARE_ERR_INVALID_ARG, "Hq=%d must be a multiple of H=%d (16384 at most)", d->Hq, d->H);
+    if (d->D < 16 || d->D > 128 || d->D % 16)
+        return fail(FLARE_ERR_UNSUPPORTED, "D=%d must be a multiple of 16 in [16, 128]", d->D);
+    if (d->page != 16 && d->page != 32 && d->page != 64 && d->page != 128)
+        return fail(FLARE_ERR_UNSUPPORTED, "page=%d must be 16, 32, 64 or 128", d->page);
+    if (d->W < 1 || (int64_t)d->W * d->page > (1ll << 30))
+        return fail(FLARE_ERR_INVALID_ARG, "W=%d: a sequence must have room for 1 to 2^30 tokens", d->W);
+    if (d->P < 1 || d->P > (1ll << 31) - 1 || d->P * d->H * d->page > (1ll << 31) - 1)
+        return fail(FLARE_ERR_INVALID_ARG, "P=%lld: the pool must hold 1 to 2^31 - 1 token rows (P*H*page)",
+                    (long long)d->P);
+    if (d->B > (1 << 20)) return fail(FLARE_ERR_UNSUPPORTED, "B=%d > 2^20", d->B);
+    if (d->dtype != FLARE_F32 && d->dtype != FLARE_BF16)
+        return fail(FLARE_ERR_INVALID_ARG, "unknown dtype %d", (int)d->dtype);
+    if (d->kernel != FLARE_KERNEL_AUTO && d->kernel != FLARE_KERNEL_SIMT && d->kernel != FLARE_KERNEL_TENSOR)
+        return fail(FLARE_ERR_INVALID_ARG, "unknown kernel family %d", (int)d->kernel);
+    if (!std::isfinite(d->scale)) return fail(FLARE_ERR_INVALID_ARG, "scale is not finite");
+    return FLARE_OK;
+}
+
+flare_status_t check_cache(const flare_cache_t *c) {
+    if (!c || !c->k || !c->v || !c->k_scale || !c->v_scale || !c->page_table)
+        return fail(FLARE_ERR_INVALID_ARG, "NULL cache tensor");
+    if (!aligned(c->k, 16) || !aligned(c->v, 16))
+        return fail(FLARE_ERR_INVALID_ARG, "the cache's codes must be 16-byte aligned");
+    if (!aligned(c->k_scale, 4) || !aligned(c->v_scale, 4) || !aligned(c->page_table, 4))
+        return fail(FLARE_ERR_INVALID_ARG, "scales and page table must be 4-byte aligned");
+    return FLARE_OK;
+}
+
+// Rows of a call: T of them, B sequences, ragged (cu) or equal.
+flare_status_t check_rows(const flare_cache_dims_t *d, int64_t T, const int32_t *lens, const int32_t *cu) {
+    if (T < 0 || T > (1ll << 31) - 1) return fail(FLARE_ERR_INVALID_ARG, "T=%lld outside [0, 2^31)", (long long)T);
+    if (!lens || !aligned(lens, 4) || !aligned(cu, 4))
+        return fail(FLARE_ERR_INVALID_ARG, "seq_lens is required, and int32 tensors must be 4-byte aligned");
+    if (!cu && d->B > 0 && T % d->B)
+        return fail(FLARE_ERR_INVALID_ARG, "T=%lld rows are not B=%d equal sequences (no cu_seqlens)", (long long)T, d->B);
+    return FLARE_OK;
+}
+
+Pool make_pool(const flare_cache_dims_t *d, const flare_cache_t *c) {
+    Pool p;
+    p.k = (uint8_t *)c->k;
+    p.v = (uint8_t *)c->v;
+    p.ks = c->k_scale;
+    p.vs = c->v_scale;
+    p.table = c->page_table;
+    p.P = d->P;
+    p.B = d->B;
+    p.H = d->H;
+    p.D = d->D;
+    p.page = d->page;
+    p.page_log2 = d->page == 16 ? 4 : d->page == 32 ? 5 : d->page == 64 ? 6 : 7;
+    p.W = d->W;
+    return p;
+}
+
+AttnPlan plan_for(const flare_cache_dims_t *d, int G, int64_t T) {
+    const flare_cache_t none = {};
+    return attn_plan(make_pool(d, &none), G, d->dtype == FLARE_BF16, T, d->kernel, planning_multiprocessors());
+}
+
+// Strides of one call's rows, in elements.
+struct Places {
+    int64_t q_sb, q_st, q_sh, o_sb, o_st, o_sh, l_sb, l_st, l_sh;
+};
+
+flare_status_t attn_run(const flare_cache_dims_t *d, const flare_cache_t *cache, int G, const void *Q,
+                        const Places &pl, int64_t T, const int32_t *lens, const int32_t *cu, int causal,
+                        void *O, bool o_f32, float *L, void *ws, size_t ws_bytes, cudaStream_t st,
+                        bool check_only) {
+    flare_status_t s;
+    if ((s = check_cache(cache)) != FLARE_OK) return s;
+    if ((s = check_rows(d, T, lens, cu)) != FLARE_OK) return s;
+    if (d->B == 0 || T == 0) return FLARE_OK;
+    if (!Q || !O) return fail(FLARE_ERR_INVALID_ARG, "NULL tensor");
+    const size_t es = elem_size(d);
+    if (!aligned(Q, es) || !aligned(O, o_f32 ? 4 : es) || !aligned(L, 4))
+        return fail(FLARE_ERR_INVALID_ARG, "tensors must be aligned to their element size");
+    const AttnPlan plan = plan_for(d, G, T);
+    if (!ws || ws_bytes < plan.bytes)
+        return fail(FLARE_ERR_WORKSPACE, "workspace of %zu bytes required, %zu given", plan.bytes, ws_bytes);
+    if (!aligned(ws, 256)) return fail(FLARE_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
+    if (check_only) return FLARE_OK;
+    AttnArgs a;
+    a.c = make_pool(d, cache);
+    a.G = G;
+    a.sl2 = (d->scale > 0.f ? d->scale : 1.0f / std::sqrt((float)d->D)) * 1.4426950408889634f;
+    a.lens = lens;
+    a.cu = cu;
+    a.n = cu ? 0 : (int)(T / d->B);
+    a.T = T;
+    a.causal = causal != 0;
+    a.Q = Q;
+    a.q_sb = pl.q_sb; a.q_st = pl.q_st; a.q_sh = pl.q_sh;
+    a.O = O;
+    a.o_sb = pl.o_sb; a.o_st = pl.o_st; a.o_sh = pl.o_sh;
+    a.L = L;
+    a.l_sb = pl.l_sb; a.l_st = pl.l_st; a.l_sh = pl.l_sh;
+    a.o_f32 = o_f32;
+    a.rows = plan.rows;
+    a.grid = plan.grid;
+    a.part_O = (float *)ws;
+    a.part_ml = (float2 *)((char *)ws + plan.part_ml);
+    a.rec = (int4 *)((char *)ws + plan.rec);
+    int sms;
+    if ((s = device_facts(&sms, &a.status)) != FLARE_OK) return s;
+    const cudaError_t e = launch_attn(a, plan.kernel, d->dtype == FLARE_BF16, st);
+    return e == cudaSuccess ? FLARE_OK
+                            : fail(FLARE_ERR_CUDA, "cache attention launch: %s", cudaGetErrorString(e));
+}
+
+flare_status_t append_run(const flare_cache_dims_t *d, const flare_cache_t *cache, const void *K,
+                          const void *V, int64_t k_stride, int64_t v_stride, int64_t T,
+                          const int32_t *lens, const int32_t *cu, const void *Q, int64_t q_stride,
+                          void *Q_out, const float *inv_freq, int rot, int interleaved,
+                          int32_t *lens_out, cudaStream_t st, bool check_only) {
+    flare_status_t s;
+    if ((s = check_cache(cache)) != FLARE_OK) return s;
+    if ((s = check_rows(d, T, lens, cu)) != FLARE_OK) return s;
+    if ((Q == nullptr) != (Q_out == nullptr))
+        return fail(FLARE_ERR_INVALID_ARG, "Q and Q_out must be given together");
+    if (Q && d->Hq < 1) return fail(FLARE_ERR_INVALID_ARG, "queries need Hq >= 1");
+    if (d->B == 0) return FLARE_OK;
+    if (T > 0 && (!K || !V)) return fail(FLARE_ERR_INVALID_ARG, "NULL tensor");
+    const size_t es = elem_size(d);
+    if (!aligned(K, es) || !aligned(V, es) || !aligned(Q, es) || !aligned(Q_out, es) || !aligned(inv_freq, 4) ||
+        !aligned(lens_out, 4))
+        return fail(FLARE_ERR_INVALID_ARG, "tensors must be aligned to their element size");
+    const int64_t hd = (int64_t)d->H * d->D, hqd = (int64_t)d->Hq * d->D;
+    if (k_stride == 0) k_stride = hd;
+    if (v_stride == 0) v_stride = hd;
+    if (q_stride == 0) q_stride = hqd;
+    if (k_stride < hd || v_stride < hd || (Q && q_stride < hqd))
+        return fail(FLARE_ERR_INVALID_ARG, "a token stride is smaller than a token's channels");
+    if (inv_freq && (rot < 2 || rot % 2 || rot > d->D))
+        return fail(FLARE_ERR_INVALID_ARG, "rot=%d must be even, from 2 to D=%d", rot, d->D);
+    if (lens_out == lens) return fail(FLARE_ERR_INVALID_ARG, "seq_lens_out may not be seq_lens");
+    if (check_only) return FLARE_OK;
+    AppendArgs a;
+    a.c = make_pool(d, cache);
+    a.K = K; a.V = V; a.Q = Q; a.Q_out = Q_out;
+    a.k_st = k_stride; a.v_st = v_stride; a.q_st = q_stride;
+    a.Hq = d->Hq;
+    a.lens = lens;
+    a.cu = cu;
+    a.n = cu ? 0 : (int)(T / d->B);
+    a.T = T;
+    a.inv_freq = inv_freq;
+    a.rot = inv_freq ? rot : 0;
+    a.inter = interleaved != 0;
+    a.lens_out = lens_out;
+    int sms;
+    if ((s = device_facts(&sms, &a.status)) != FLARE_OK) return s;
+    const cudaError_t e = launch_append(a, d->dtype == FLARE_BF16, st);
+    return e == cudaSuccess ? FLARE_OK : fail(FLARE_ERR_CUDA, "cache append launch: %s", cudaGetErrorString(e));
+}
+
+flare_status_t encoder_run(const flare_cache_dims_t *d, const flare_cache_t *cache, int M, const void *Q,
+                           int64_t q_batch_stride, const int32_t *lens, float *Z, float *L, void *ws,
+                           size_t ws_bytes, cudaStream_t st, bool check_only) {
+    const int64_t hmd = (int64_t)d->H * M * d->D;
+    if (M < 1 || M > (1 << 20)) return fail(FLARE_ERR_INVALID_ARG, "M=%d outside [1, 2^20]", M);
+    if (q_batch_stride != 0 && q_batch_stride != hmd)
+        return fail(FLARE_ERR_INVALID_ARG, "q_batch_stride must be 0 or H*M*D (%lld)", (long long)hmd);
+    if (d->B > 0 && !L) return fail(FLARE_ERR_INVALID_ARG, "NULL tensor");
+    const int64_t md = (int64_t)M * d->D;
+    const Places pl{q_batch_stride, d->D, md, hmd, d->D, md, (int64_t)d->H * M, 1, M};
+    return attn_run(d, cache, 1, Q, pl, (int64_t)d->B * M, lens, nullptr, 0, Z, true, L, ws, ws_bytes, st,
+                    check_only);
+}
+
+}  // namespace
+}  // namespace flare
+
+using namespace flare;
+
+extern "C" {
+
+flare_status_t flare_cache_append(const flare_cache_dims_t *dims, const flare_cache_t *cache, const void *K,
+                                  const void *V, int64_t k_stride, int64_t v_stride, int64_t T,
+                                  const int32_t *seq_lens, const int32_t *cu_seqlens, const void *Q,
+                                  int64_t q_stride, void *Q_out, const float *inv_freq, int rot,
+                                  int interleaved, int32_t *seq_lens_out, void *stream) {
+    FLARE_TRACE();
+    const flare_status_t s = check_dims(dims);
+    if (s != FLARE_OK) return s;
+    return append_run(dims, cache, K, V, k_stride, v_stride, T, seq_lens, cu_seqlens, Q, q_stride, Q_out,
+                      inv_freq, rot, interleaved, seq_lens_out, (cudaStream_t)stream, false);
+}
+
+size_t flare_cache_workspace_bytes(const flare_cache_dims_t *dims, int64_t T) {
+    if (check_dims(dims) != FLARE_OK) return (size_t)-1;
+    if (dims->Hq < 1 || T < 0 || T > (1ll << 31) - 1) {
+        fail(FLARE_ERR_INVALID_ARG, "Hq=%d, T=%lld: no query rows", dims->Hq, (long long)T);
+        return (size_t)-1;
+    }
+    return T == 0 || dims->B == 0 ? 0 : plan_for(dims, dims->Hq / dims->H, T).bytes;
+}
+
+flare_status_t flare_cache_attn(const flare_cache_dims_t *dims, const flare_cache_t *cache, const void *Q,
+                                int64_t q_stride, int64_t T, const int32_t *seq_lens,
+                                const int32_t *cu_seqlens, int causal, void *O, float *L, void *workspace,
+                                size_t workspace_bytes, void *stream) {
+    FLARE_TRACE();
+    const flare_status_t s = check_dims(dims);
+    if (s != FLARE_OK) return s;
+    if (dims->Hq < 1) return fail(FLARE_ERR_INVALID_ARG, "Hq must be >= 1");
+    const int64_t hqd = (int64_t)dims->Hq * dims->D;
+    if (q_stride == 0) q_stride = hqd;
+    if (q_stride < hqd) return fail(FLARE_ERR_INVALID_ARG, "q_stride is smaller than a token's channels");
+    const Places pl{-1, q_stride, dims->D, -1, hqd, dims->D, -1, dims->Hq, 1};
+    return attn_run(dims, cache, dims->Hq / dims->H, Q, pl, T, seq_lens, cu_seqlens, causal, O, false, L,
+                    workspace, workspace_bytes, (cudaStream_t)stream, false);
+}
+
+flare_status_t flare_cache_encoder_fwd(const flare_cache_dims_t *dims, const flare_cache_t *cache, int M,
+                                       const void *Q, int64_t q_batch_stride, const int32_t *seq_lens,
+                                       float *Z, float *L, void *workspace, size_t workspace_bytes,
+                                       void *stream) {
+    FLARE_TRACE();
+    const flare_status_t s = check_dims(dims);
+    if (s != FLARE_OK) return s;
+    return encoder_run(dims, cache, M, Q, q_batch_stride, seq_lens, Z, L, workspace, workspace_bytes,
+                       (cudaStream_t)stream, false);
+}
+
+flare_status_t flare_cache_fwd(const flare_cache_dims_t *dims, const flare_cache_t *cache, int M, int N,
+                               const void *Q, int64_t q_batch_stride, const void *K, const void *V,
+                               const int32_t *seq_lens, int32_t *seq_lens_out, void *Y, float *Z, float *L,
+                               void *workspace, size_t workspace_bytes, void *stream) {
+    FLARE_TRACE();
+    flare_status_t s = check_dims(dims);
+    if (s != FLARE_OK) return s;
+    if (N < 0) return fail(FLARE_ERR_INVALID_ARG, "N must be >= 0");
+    if (!seq_lens_out) return fail(FLARE_ERR_INVALID_ARG, "seq_lens_out is required");
+    flare_dims_t dec = {};
+    dec.B = dims->B;
+    dec.H = dims->H;
+    dec.M = M;
+    dec.N = N;
+    dec.D = dims->D;
+    dec.scale = dims->scale;
+    dec.dtype = dims->dtype;
+    dec.q_batch_stride = q_batch_stride;
+    dec.kernel = dims->kernel == FLARE_KERNEL_TENSOR ? FLARE_KERNEL_AUTO : dims->kernel;
+    cudaStream_t st = (cudaStream_t)stream;
+    // the three stages' arguments are checked before the first launch
+    for (const bool check : {true, false}) {
+        if ((s = append_run(dims, cache, K, V, 0, 0, (int64_t)dims->B * N, seq_lens, nullptr, nullptr, 0, nullptr,
+                            nullptr, 0, 0, seq_lens_out, st, check)) != FLARE_OK)
+            return s;
+        if ((s = encoder_run(dims, cache, M, Q, q_batch_stride, seq_lens_out, Z, L, workspace, workspace_bytes,
+                             st, check)) != FLARE_OK)
+            return s;
+        if ((s = decode_with(&dec, Q, Z, K, Y, st, check)) != FLARE_OK) return s;
+    }
+    return FLARE_OK;
+}
+
+}  // extern "C"

@@ -1,0 +1,279 @@
+// cache_attn.cu -- attention over the paged 8-bit cache: the CUDA-core kernel,
+// the merge of cut items, and the choice of a kernel.
+//
+// For a query row q of shared head h and the tokens n it sees:
+//   S_n = s <q, k_n>,  L = log sum_n exp(S_n),  O = sum_n exp(S_n - L) v_n,
+// with k_n, v_n the codes times their page's scales. A running maximum m and
+// sum l (fp32) carry the softmax over the tokens in one pass.
+#include "cache_device.cuh"
+
+namespace flare {
+namespace cache {
+
+// ---- CUDA cores -----------------------------------------------------------------
+// R rows a tile, four warps; each warp takes 32 of a tile's 128 tokens, one
+// token a lane for S = Q K^T (a lane reads its whole key row, 16 bytes at a
+// time; Q is broadcast from shared memory), then four channels a lane for
+// O += P V (a warp reads a value row, 4 bytes a lane). Every product is an
+// fp32 FMA on exactly converted codes. The reads are as few as they can be
+// for one head's rows; the FMAs bound it from some four rows on.
+template <int R, bool BF16>
+__global__ void __launch_bounds__(128) attn_simt_kernel(const AttnArgs a) {
+    constexpr int NT = 128, NW = 4;
+    __shared__ int64_t scan_sh[NW];
+    __shared__ Cursor cur_sh;
+    __shared__ __align__(16) float q_sh[R][128];
+    __shared__ __align__(16) float p_sh[NW][R][32];
+    __shared__ __align__(16) float o_sh[NW][R][128];
+    __shared__ float m_sh[NW][R], l_sh[NW][R];
+    const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5, cta = blockIdx.x;
+    const int D = a.c.D;
+    const Span sp = find_span<NT>(a, cta, scan_sh, &cur_sh);
+    Cursor cur = cur_sh;
+    if (tid == 0) write_record(a, sp, cur, cta);
+    while (cur.tiles_left > 0) {
+        const int k0 = cur.k, k1 = imin(cur.nt, cur.k + cur.tiles_left);
+        __syncthreads();
+        int limit[R];
+#pragma unroll
+        for (int r = 0; r < R; ++r) limit[r] = row_place(a, cur.s, cur.b, cur.rt, cur.h, r).limit;
+        for (int i = tid; i < R * D; i += NT) {
+            const int r = i / D, d = i - r * D;
+            const RowPlace p = row_place(a, cur.s, cur.b, cur.rt, cur.h, r);
+            q_sh[r][d] = p.valid ? load_q(a, BF16, p.q + d) : 0.f;
+        }
+        __syncthreads();
+        float m[R], l[R];
+        float4 o[R];
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            m[r] = -INFINITY;
+            l[r] = 0.f;
+            o[r] = make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+        const int seen = visible(cur.s, a.G, a.rows, cur.rt, a.causal);
+        for (int k = k0; k < k1; ++k) {
+            const int n0 = k * kTile + 32 * w, n = n0 + lane;
+            if (n0 >= seen) continue;
+            const int page = n < seen ? page_of(a.c, cur.b, n, a.status) : -1;
+            const int64_t ph = (int64_t)page * a.c.H + cur.h;
+            const int64_t row = (ph * a.c.page + (n & (a.c.page - 1))) * D;
+            float s[R];
+#pragma unroll
+            for (int r = 0; r < R; ++r) s[r] = 0.f;
+            float vs = 0.f, t_scale = 0.f;
+            if (page >= 0) {
+                t_scale = a.c.ks[ph] * a.sl2;
+                vs = a.c.vs[ph];
+                for (int d = 0; d < D; d += 16) {
+                    const uint4 kq = *reinterpret_cast<const uint4 *>(a.c.k + row + d);
+                    const uint32_t kw[4] = {kq.x, kq.y, kq.z, kq.w};
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        const float2 x = float2_of(f16x2_of_e4m3x2(kw[c]));
+                        const float2 y = float2_of(f16x2_of_e4m3x2_hi(kw[c]));
+#pragma unroll
+                        for (int r = 0; r < R; ++r) {
+                            const float4 q = *reinterpret_cast<const float4 *>(&q_sh[r][d + 4 * c]);
+                            s[r] = fmaf(q.x, x.x, s[r]);
+                            s[r] = fmaf(q.y, x.y, s[r]);
+                            s[r] = fmaf(q.z, y.x, s[r]);
+                            s[r] = fmaf(q.w, y.y, s[r]);
+                        }
+                    }
+                }
+            }
+            // (a lane's value scale goes into its weight for O, not into the sum)
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                const float t = page >= 0 && n < limit[r] ? s[r] * t_scale : -INFINITY;
+                float mx = t;
+#pragma unroll
+                for (int x = 16; x; x >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, x));
+                const float mn = fmaxf(m[r], mx);
+                const float ref = mn == -INFINITY ? 0.f : mn;
+                const float f = exp2f(m[r] - ref);           // m = -inf: 0
+                const float p = exp2f(t - ref);
+                m[r] = mn;
+                l[r] = l[r] * f + p;
+                o[r].x *= f; o[r].y *= f; o[r].z *= f; o[r].w *= f;
+                p_sh[w][r][lane] = p * vs;
+            }
+            __syncwarp();
+            const int cnt = imin(32, seen - n0);
+            for (int j = 0; j < cnt; ++j) {
+                const int64_t vrow = __shfl_sync(0xffffffffu, row, j);
+                const int vpage = __shfl_sync(0xffffffffu, page, j);
+                if (vpage >= 0 && 4 * lane < D) {
+                    const uint32_t c = *reinterpret_cast<const uint32_t *>(a.c.v + vrow + 4 * lane);
+                    const float2 x = float2_of(f16x2_of_e4m3x2(c)), y = float2_of(f16x2_of_e4m3x2_hi(c));
+#pragma unroll
+                    for (int r = 0; r < R; ++r) {
+                        const float p = p_sh[w][r][j];
+                        o[r].x = fmaf(p, x.x, o[r].x);
+                        o[r].y = fmaf(p, x.y, o[r].y);
+                        o[r].z = fmaf(p, y.x, o[r].z);
+                        o[r].w = fmaf(p, y.y, o[r].w);
+                    }
+                }
+            }
+            __syncwarp();
+        }
+        // the four warps' states of each row become one
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            float x = l[r];
+#pragma unroll
+            for (int s = 16; s; s >>= 1) x += __shfl_xor_sync(0xffffffffu, x, s);
+            if (lane == 0) {
+                m_sh[w][r] = m[r];
+                l_sh[w][r] = x;
+            }
+            if (4 * lane < D) *reinterpret_cast<float4 *>(&o_sh[w][r][4 * lane]) = o[r];
+        }
+        __syncthreads();
+        const bool whole = k0 == 0 && k1 == cur.nt;
+        const int64_t slot = (int64_t)cta * 2 + (k0 == 0 ? 1 : 0);
+        for (int r = w; r < R; r += NW) {
+            const RowPlace p = row_place(a, cur.s, cur.b, cur.rt, cur.h, r);
+            if (!p.valid) continue;
+            float M = -INFINITY, ls = 0.f;
+#pragma unroll
+            for (int x = 0; x < NW; ++x) M = fmaxf(M, m_sh[x][r]);
+            const float ref = M == -INFINITY ? 0.f : M;
+            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int x = 0; x < NW; ++x) {
+                const float f = exp2f(m_sh[x][r] - ref);
+                ls += l_sh[x][r] * f;
+                if (4 * lane < D) {
+                    const float4 y = *reinterpret_cast<const float4 *>(&o_sh[x][r][4 * lane]);
+                    v.x = fmaf(f, y.x, v.x); v.y = fmaf(f, y.y, v.y);
+                    v.z = fmaf(f, y.z, v.z); v.w = fmaf(f, y.w, v.w);
+                }
+            }
+            if (whole) {
+                const float inv = ls == 0.f ? 0.f : 1.f / ls;
+                if (4 * lane < D)
+                    store_o4(a, !BF16 || a.o_f32, p.o + 4 * lane,
+                             make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv));
+                if (a.L && lane == 0) a.L[p.l] = ls == 0.f ? -INFINITY : (ref + log2f(ls)) * kLn2;
+            } else {
+                if (4 * lane < D)
+                    *reinterpret_cast<float4 *>(&a.part_O[(slot * a.rows + r) * D + 4 * lane]) = v;
+                if (lane == 0) a.part_ml[slot * a.rows + r] = make_float2(ref, ls);
+            }
+        }
+        cur.tiles_left -= k1 - k0;
+        if (cur.tiles_left > 0) next_item(a, cur);
+    }
+    tc::pdl_launch_dependents();
+}
+
+// ---- merge --------------------------------------------------------------------------
+// One warp a row of the item that ends in span blockIdx.x: its pieces lie in
+// spans first .. blockIdx.x, the first in slot 1 (it began there) and the rest
+// in slot 0. They are added in that order, so results do not vary. A piece
+// without a visible token has l = 0. Bound by latency: a few KB a row.
+__global__ void __launch_bounds__(128) attn_merge_kernel(const AttnArgs a, const int f32) {
+    tc::pdl_wait();
+    const int4 rec = a.rec[blockIdx.x];
+    if (rec.x < 0) return;
+    const int lane = threadIdx.x & 31, r = blockIdx.y * 4 + (threadIdx.x >> 5);
+    const int D = a.c.D, first = rec.w, count = (int)blockIdx.x - first + 1;
+    if (r >= a.rows) return;
+    const Seq s = load_seq(a, rec.x);
+    const RowPlace p = row_place(a, s, rec.x, rec.y, rec.z, r);
+    if (!p.valid) return;
+    auto slot = [&](int i) { return ((int64_t)(first + i) * 2 + (i == 0 ? 1 : 0)) * a.rows + r; };
+    float M = -INFINITY;
+    for (int i = lane; i < count; i += 32) {
+        const float2 ml = a.part_ml[slot(i)];
+        if (!(ml.y == 0.f)) M = fmaxf(M, ml.x);
+    }
+#pragma unroll
+    for (int x = 16; x; x >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, x));
+    const float ref = M == -INFINITY ? 0.f : M;
+    float l = 0.f;
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int base = 0; base < count; base += 32) {
+        float f = 0.f;
+        if (base + lane < count) {
+            const float2 ml = a.part_ml[slot(base + lane)];
+            f = ml.y == 0.f ? 0.f : tc::ex2(ml.x - ref);
+            l += f * ml.y;
+        }
+        const int m = imin(32, count - base);
+#pragma unroll 4
+        for (int i = 0; i < m; ++i) {
+            const float g = __shfl_sync(0xffffffffu, f, i);
+            if (4 * lane < D) {
+                const float4 y = *reinterpret_cast<const float4 *>(&a.part_O[slot(base + i) * D + 4 * lane]);
+                v.x = fmaf(g, y.x, v.x); v.y = fmaf(g, y.y, v.y);
+                v.z = fmaf(g, y.z, v.z); v.w = fmaf(g, y.w, v.w);
+            }
+        }
+    }
+#pragma unroll
+    for (int x = 16; x; x >>= 1) l += __shfl_xor_sync(0xffffffffu, l, x);
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    if (4 * lane < D)
+        store_o4(a, f32 != 0, p.o + 4 * lane, make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv));
+    if (a.L && lane == 0) a.L[p.l] = l == 0.f ? -INFINITY : (ref + log2f(l)) * kLn2;
+}
+
+// ---- choice and launch ----------------------------------------------------------------
+AttnPlan attn_plan(const Pool &c, int G, bool bf16, int64_t T, int family, int sms) {
+    AttnPlan p;
+    p.kernel = AttnKernel::kSimt;
+    p.rows = 8;
+    int64_t grid = (int64_t)sms * 4;
+    // no more spans than there can be tiles
+    const int64_t tiles = ((T * G + p.rows - 1) / p.rows + c.B) * c.H *
+                          (((int64_t)c.W * c.page + kTile - 1) / kTile + 1);
+    if (grid > tiles) grid = tiles;
+    p.grid = (int)(grid < 1 ? 1 : grid);
+    auto up = [](size_t x) { return (x + 255) & ~(size_t)255; };
+    size_t o = up(sizeof(float) * 2 * p.grid * p.rows * c.D);
+    p.part_ml = o;
+    o += up(sizeof(float2) * 2 * p.grid * p.rows);
+    p.rec = o;
+    o += up(sizeof(int4) * p.grid);
+    p.bytes = o;
+    return p;
+}
+
+namespace {
+template <typename Kernel, typename... Args>
+cudaError_t launch_pdl(Kernel k, dim3 grid, dim3 block, cudaStream_t st, Args... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, k, args...);
+}
+}  // namespace
+
+cudaError_t launch_attn(const AttnArgs &a, AttnKernel kernel, bool bf16, cudaStream_t st) {
+    (void)kernel;
+    if (bf16)
+        attn_simt_kernel<8, true><<<a.grid, 128, 0, st>>>(a);
+    else
+        attn_simt_kernel<8, false><<<a.grid, 128, 0, st>>>(a);
+    note_launch();
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    e = launch_pdl(attn_merge_kernel, dim3(a.grid, (a.rows + 3) / 4), dim3(128), st, a,
+                   (int)(!bf16 || a.o_f32));
+    if (e != cudaSuccess) return e;
+    note_launch();
+    return cudaGetLastError();
+}
+
+}  // namespace cache
+}  // namespace flare

@@ -1,0 +1,75 @@
+// cache_common.cuh -- declarations shared by the kernels of the paged 8-bit
+// token cache and their launchers.
+#pragma once
+
+#include "cache_plan.cuh"
+#include "flare_internal.cuh"
+
+namespace flare {
+namespace cache {
+
+// Device status word: a page number outside the pool, a length outside the
+// page table or offsets outside the token rows (the access was skipped).
+enum : unsigned { kDevBadCache = 2 };
+
+struct Pool {
+    uint8_t *k, *v;             // e4m3 codes [P, H, page, D]
+    float *ks, *vs;             // [P, H]
+    const int32_t *table;       // [B, W]
+    int64_t P;
+    int B, H, D, page, page_log2, W;
+};
+
+struct AttnArgs {
+    Pool c;
+    int G;                              // query heads of one cache head
+    float sl2;                          // score scale * log2(e)
+    const int32_t *lens, *cu;
+    int n;                              // rows a sequence where cu is null
+    int64_t T;
+    int causal;
+    const void *Q;                      // element (b, i, hq, d) at b*q_sb + i*q_st + hq*q_sh + d
+    int64_t q_sb, q_st, q_sh;           // q_sb < 0: rows t0 + i of a ragged call, t*q_st
+    void *O;
+    int64_t o_sb, o_st, o_sh;
+    float *L;                           // may be null
+    int64_t l_sb, l_st, l_sh;
+    int o_f32;                          // O is fp32 although Q is bf16
+    int rows;                           // rows of one row tile
+    int grid;                           // spans at most
+    // workspace: a span's unfinished pieces, two at most (see write_piece)
+    float *part_O;                      // [grid][2][rows][D]
+    float2 *part_ml;                    // [grid][2][rows]
+    int4 *rec;                          // [grid][2]: the item whose last piece a span holds
+    unsigned *status;
+};
+
+struct AppendArgs {
+    Pool c;
+    const void *K, *V, *Q;
+    void *Q_out;
+    int64_t k_st, v_st, q_st;           // elements between tokens
+    int Hq;
+    const int32_t *lens, *cu;
+    int n;
+    int64_t T;
+    const float *inv_freq;
+    int rot, inter;
+    int32_t *lens_out;
+    unsigned *status;
+};
+
+// Which kernel takes an attention call, and what it needs.
+enum class AttnKernel { kSimt, kMma, kTc };
+struct AttnPlan {
+    AttnKernel kernel;
+    int rows, grid;
+    size_t part_ml, rec, bytes;         // workspace: part_O at 0
+};
+AttnPlan attn_plan(const Pool &c, int G, bool bf16, int64_t T, int family, int sms);
+
+cudaError_t launch_attn(const AttnArgs &a, AttnKernel kernel, bool bf16, cudaStream_t st);
+cudaError_t launch_append(const AppendArgs &a, bool bf16, cudaStream_t st);
+
+}  // namespace cache
+}  // namespace flare

@@ -1,0 +1,211 @@
+// cache_device.cuh -- device code shared by the attention kernels over the
+// paged 8-bit cache: a worker's span of the work, the places of its rows, the
+// pages of its tokens, and where its results go.
+//
+// Work: the items (sequence b, row tile rt, cache head h), in that order with
+// h innermost, are each cut into tiles of kTile tokens; the tiles of all items
+// in a row are dealt out to the workers (CTAs) in equal contiguous spans, so
+// that one long sequence among short ones is shared by all of them. Lengths
+// are device data: every CTA adds up the tiles for itself (one pass over the
+// B lengths). An item that lies in one span is finished there; one that is cut
+// leaves a partial (O, m, l) in each span and the merge kernel adds them up.
+#pragma once
+
+#include "cache_common.cuh"
+#include "tc_ptx.cuh"
+
+#include <cuda_fp16.h>
+
+namespace flare {
+namespace cache {
+
+constexpr float kLn2 = 0.69314718055994531f;
+
+__device__ __forceinline__ void flag_bad(unsigned *status) { atomicCAS(status, 0u, (unsigned)kDevBadCache); }
+
+__device__ __forceinline__ Seq load_seq(const AttnArgs &a, int b) {
+    return sequence(a.cu, a.n, a.T, a.lens, a.c.W * a.c.page, b);
+}
+
+// ---- span ------------------------------------------------------------------
+struct Cursor {
+    int b, rt, h, k, nt, tiles_left;     // tile k of nt of the item; tiles of the span left
+    Seq s;
+};
+struct Span {
+    int64_t begin, total;
+    int parts;                           // spans in use
+};
+
+// One block-wide sum (and exclusive prefix) of an int64 per thread.
+template <int NT>
+__device__ __forceinline__ int64_t block_scan(int64_t v, int64_t *sh, int64_t &total) {
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+    int64_t x = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+    }
+    __syncthreads();
+    if (lane == 31) sh[w] = x;
+    __syncthreads();
+    int64_t base = 0;
+    total = 0;
+#pragma unroll
+    for (int i = 0; i < NT / 32; ++i) {
+        if (i < w) base += sh[i];
+        total += sh[i];
+    }
+    return base + x - v;
+}
+
+// The span of CTA `c` and the cursor at its first tile. Every thread of the
+// block calls it; sh: NT / 32 int64, found: one Cursor, in shared memory.
+// An empty span leaves tiles_left = 0.
+template <int NT>
+__device__ __forceinline__ Span find_span(const AttnArgs &a, int c, int64_t *sh, Cursor *found) {
+    const int tid = threadIdx.x, B = a.c.B;
+    Span sp;
+    sp.total = 0;
+    int64_t first = 0;                   // this thread's tiles in the first block of sequences
+    for (int base = 0; base < B; base += NT) {
+        int64_t v = 0, sum;
+        if (base + tid < B) {
+            const Seq s = load_seq(a, base + tid);
+            if (!s.ok && c == 0) flag_bad(a.status);
+            v = seq_tiles(s, a.G, a.rows, a.causal) * a.c.H;
+        }
+        if (base == 0) first = v;
+        block_scan<NT>(v, sh, sum);
+        sp.total += sum;
+    }
+    sp.parts = (int)lmin(a.grid, sp.total);
+    if (tid == 0) found->tiles_left = 0;
+    if (c >= sp.parts) {
+        sp.begin = sp.total;
+        __syncthreads();
+        return sp;
+    }
+    sp.begin = span_begin(sp.total, sp.parts, c);
+    const int64_t end = span_begin(sp.total, sp.parts, c + 1);
+    int64_t before = 0;
+    for (int base = 0; base < B; base += NT) {
+        int64_t v = first, sum;
+        if (base > 0) {
+            v = 0;
+            if (base + tid < B) v = seq_tiles(load_seq(a, base + tid), a.G, a.rows, a.causal) * a.c.H;
+        }
+        int64_t at = before + block_scan<NT>(v, sh, sum);
+        if (v > 0 && at <= sp.begin && sp.begin < at + v) {
+            Cursor cur;
+            cur.b = base + tid;
+            cur.s = load_seq(a, cur.b);
+            cur.rt = 0;
+            while (true) {
+                cur.nt = item_tiles(cur.s, a.G, a.rows, cur.rt, a.causal);
+                if (sp.begin < at + (int64_t)cur.nt * a.c.H) break;
+                at += (int64_t)cur.nt * a.c.H;
+                ++cur.rt;
+            }
+            const int64_t off = sp.begin - at;
+            cur.h = (int)(off / cur.nt);
+            cur.k = (int)(off - (int64_t)cur.h * cur.nt);
+            cur.tiles_left = (int)(end - sp.begin);
+            *found = cur;
+        }
+        before += sum;
+        if (before > sp.begin) break;    // the same for every thread
+    }
+    __syncthreads();
+    return sp;
+}
+
+// The next item after `cur` (called only while tiles of the span are left).
+__device__ __forceinline__ void next_item(const AttnArgs &a, Cursor &cur) {
+    cur.k = 0;
+    if (++cur.h < a.c.H) return;
+    cur.h = 0;
+    ++cur.rt;
+    while (cur.rt >= row_tiles(cur.s, a.G, a.rows)) {
+        if (++cur.b >= a.c.B) return;
+        cur.s = load_seq(a, cur.b);
+        cur.rt = 0;
+    }
+    cur.nt = item_tiles(cur.s, a.G, a.rows, cur.rt, a.causal);
+}
+
+// Which item's last piece CTA c holds, for the merge: (b, rt, h, first CTA),
+// or b = -1. It can only be the first piece of its span.
+__device__ __forceinline__ void write_record(const AttnArgs &a, const Span &sp, const Cursor &cur, int c) {
+    int4 r = make_int4(-1, 0, 0, 0);
+    if (cur.tiles_left > 0 && cur.k > 0 && cur.k + cur.tiles_left >= cur.nt)
+        r = make_int4(cur.b, cur.rt, cur.h, part_of(sp.total, sp.parts, sp.begin - cur.k));
+    a.rec[c] = r;
+}
+
+// ---- rows ------------------------------------------------------------------
+struct RowPlace {
+    bool valid;
+    int limit;                           // tokens it sees
+    int64_t q, o, l;                     // element offsets
+};
+__device__ __forceinline__ RowPlace row_place(const AttnArgs &a, const Seq &s, int b, int rt, int h, int row) {
+    RowPlace p;
+    const int64_t rr = (int64_t)rt * a.rows + row;
+    p.valid = rr < (int64_t)s.n * a.G;
+    const int i = p.valid ? (int)(rr / a.G) : 0;
+    const int hq = h * a.G + (p.valid ? (int)(rr - (int64_t)i * a.G) : 0);
+    p.limit = p.valid ? limit_of(s, i, a.causal) : 0;
+    p.q = (a.q_sb < 0 ? (s.t0 + i) * a.q_st : b * a.q_sb + i * a.q_st) + hq * a.q_sh;
+    p.o = (a.o_sb < 0 ? (s.t0 + i) * a.o_st : b * a.o_sb + i * a.o_st) + hq * a.o_sh;
+    p.l = (a.l_sb < 0 ? (s.t0 + i) * a.l_st : b * a.l_sb + i * a.l_st) + hq * a.l_sh;
+    return p;
+}
+
+// Page that holds token n of sequence b, or -1 (and the status word set) where
+// the table names none of the pool.
+__device__ __forceinline__ int page_of(const Pool &c, int b, int n, unsigned *status) {
+    const int p = c.table[(int64_t)b * c.W + (n >> c.page_log2)];
+    if (p < 0 || p >= c.P) {
+        flag_bad(status);
+        return -1;
+    }
+    return p;
+}
+
+__device__ __forceinline__ float load_q(const AttnArgs &a, bool bf16, int64_t at) {
+    return bf16 ? __bfloat162float(reinterpret_cast<const __nv_bfloat16 *>(a.Q)[at])
+                : reinterpret_cast<const float *>(a.Q)[at];
+}
+
+// 4 output channels d .. d+3 of a row.
+__device__ __forceinline__ void store_o4(const AttnArgs &a, bool f32, int64_t at, float4 v) {
+    if (f32) {
+        float *o = reinterpret_cast<float *>(a.O) + at;
+        o[0] = v.x; o[1] = v.y; o[2] = v.z; o[3] = v.w;
+    } else {
+        __nv_bfloat16 *o = reinterpret_cast<__nv_bfloat16 *>(a.O) + at;
+        o[0] = __float2bfloat16_rn(v.x); o[1] = __float2bfloat16_rn(v.y);
+        o[2] = __float2bfloat16_rn(v.z); o[3] = __float2bfloat16_rn(v.w);
+    }
+}
+
+// e4m3 codes (two in the low half of x) as two fp16: exact.
+__device__ __forceinline__ uint32_t f16x2_of_e4m3x2(uint32_t x) {
+    uint32_t r;
+    asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, lo;\n\t}" : "=r"(r) : "r"(x));
+    return r;
+}
+// The same of the two codes in the high half.
+__device__ __forceinline__ uint32_t f16x2_of_e4m3x2_hi(uint32_t x) {
+    uint32_t r;
+    asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, hi;\n\t}" : "=r"(r) : "r"(x));
+    return r;
+}
+__device__ __forceinline__ float2 float2_of(uint32_t h2) {
+    return __half22float2(*reinterpret_cast<__half2 *>(&h2));
+}
+
+}  // namespace cache
+}  // namespace flare

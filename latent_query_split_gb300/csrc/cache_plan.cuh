@@ -1,0 +1,105 @@
+// cache_plan.cuh -- index arithmetic of the paged 8-bit token cache, for host
+// and device: where a sequence's tokens and pages are, how the attention's
+// work is cut into equal spans, which pages an append touches. No CUDA types,
+// so that it also compiles as plain C++ (the CPU tests do).
+#pragma once
+
+#include <stdint.h>
+
+#ifdef __CUDACC__
+#define FLARE_HD __host__ __device__ __forceinline__
+#else
+#define FLARE_HD inline
+#endif
+
+namespace flare {
+namespace cache {
+
+constexpr int kTile = 128;       // tokens of one tile of the attention's work
+
+FLARE_HD int imin(int a, int b) { return a < b ? a : b; }
+FLARE_HD int imax(int a, int b) { return a > b ? a : b; }
+FLARE_HD int64_t lmin(int64_t a, int64_t b) { return a < b ? a : b; }
+
+// One sequence of a call: its query (or new) tokens [t0, t0 + n) of the call's
+// T token rows and the `len` tokens it holds in the cache.
+struct Seq {
+    int64_t t0;
+    int n, len;
+    bool ok;      // lengths and offsets were in range (they are clamped otherwise)
+};
+
+// cu: B + 1 offsets of the sequences' rows, or null: n rows each. Everything
+// read from device memory is clamped into range, so that no later index can
+// leave its buffer; `ok` says whether it had to be.
+FLARE_HD Seq sequence(const int32_t *cu, int n, int64_t T, const int32_t *lens, int capacity, int b) {
+    Seq s;
+    s.ok = true;
+    if (cu) {
+        const int64_t lo = cu[b], hi = cu[b + 1];
+        s.t0 = lo < 0 ? 0 : lmin(lo, T);
+        const int64_t end = hi < s.t0 ? s.t0 : lmin(hi, T);
+        s.n = (int)(end - s.t0);
+        s.ok = lo >= 0 && hi >= lo && hi <= T;
+    } else {
+        s.t0 = (int64_t)b * n;
+        s.n = n;
+    }
+    const int len = lens[b];
+    s.len = imax(0, imin(len, capacity));
+    s.ok = s.ok && s.len == len;
+    return s;
+}
+
+// ---- attention ---------------------------------------------------------------
+// Row r of a sequence and shared head is query token r / G, query head
+// h * G + r % G. Rows are taken `rows` at a time (row tiles); a row tile sees
+// the tokens [0, visible()) at most.
+FLARE_HD int row_tiles(const Seq &s, int G, int rows) {
+    return (int)(((int64_t)s.n * G + rows - 1) / rows);
+}
+FLARE_HD int visible(const Seq &s, int G, int rows, int rt, bool causal) {
+    if (!causal) return s.len;
+    const int64_t last = ((int64_t)(rt + 1) * rows - 1) / G;      // last query token of the tile
+    const int64_t i = lmin(last, s.n - 1);
+    const int64_t seen = (int64_t)s.len - s.n + i + 1;
+    return (int)(seen < 0 ? 0 : seen);
+}
+// Tokens that query token i sees.
+FLARE_HD int limit_of(const Seq &s, int i, bool causal) {
+    if (!causal) return s.len;
+    const int64_t seen = (int64_t)s.len - s.n + i + 1;
+    return (int)(seen < 0 ? 0 : seen);
+}
+// Tiles of one (row tile, head): one at least, so that somebody writes the
+// rows that see nothing.
+FLARE_HD int item_tiles(const Seq &s, int G, int rows, int rt, bool causal) {
+    return imax(1, (visible(s, G, rows, rt, causal) + kTile - 1) / kTile);
+}
+// Tiles of one head over the row tiles of a sequence.
+FLARE_HD int64_t seq_tiles(const Seq &s, int G, int rows, bool causal) {
+    const int m = row_tiles(s, G, rows);
+    if (!causal) return m > 0 ? (int64_t)m * item_tiles(s, G, rows, 0, false) : 0;
+    int64_t sum = 0;
+    for (int rt = 0; rt < m; ++rt) sum += item_tiles(s, G, rows, rt, true);
+    return sum;
+}
+
+// Equal spans of `total` tiles for `parts` workers (parts <= total).
+FLARE_HD int64_t span_begin(int64_t total, int parts, int c) {
+    return ((int64_t)c * total + parts - 1) / parts;
+}
+FLARE_HD int part_of(int64_t total, int parts, int64_t t) { return (int)(t * parts / total); }
+
+// ---- append -------------------------------------------------------------------
+// A sequence's touched pages get the numbers first_slot(b) + 0, 1, ...; the
+// numbers of different sequences do not meet, because n tokens touch at most
+// floor(n / page) + 2 pages.
+FLARE_HD int64_t first_slot(int64_t t0, int b, int page) { return t0 / page + 2 * (int64_t)b; }
+FLARE_HD int64_t slot_bound(int64_t T, int B, int page) { return T / page + 2 * (int64_t)B; }
+FLARE_HD int touched_pages(int len, int n, int page) {
+    return n > 0 ? (int)(((int64_t)len + n - 1) / page - len / page + 1) : 0;
+}
+
+}  // namespace cache
+}  // namespace flare

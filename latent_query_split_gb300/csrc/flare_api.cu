@@ -485,6 +485,23 @@ flare_status_t encoder_fwd_with_workspace(const flare_dims_t *dims, const void *
 
 flare_status_t report_error(flare_status_t s, const char *msg) { return fail(s, "%s", msg); }
 
+flare_status_t device_facts(int *sms, unsigned **status) {
+    DeviceInfo d;
+    const flare_status_t s = device_info(d);
+    if (s != FLARE_OK) return s;
+    *sms = d.sms;
+    *status = d.status;
+    return FLARE_OK;
+}
+
+int planning_multiprocessors() { return planning_sms(); }
+
+flare_status_t decode_with(const flare_dims_t *dims, const void *Q, const float *Z, const void *K, void *Y,
+                           cudaStream_t st, bool check_only) {
+    const flare_status_t s = check_dims(dims);
+    return s != FLARE_OK ? s : decode_run(dims, Q, false, Z, K, Y, false, st, check_only);
+}
+
 }  // namespace flare
 
 using namespace flare;
@@ -748,6 +765,9 @@ flare_status_t flare_device_status(void *stream) {
     if (v != kDevOk) {
         const unsigned zero = 0;
         cudaMemcpyToSymbol(g_device_status, &zero, sizeof zero);
+        if (v == 2u)
+            return fail(FLARE_ERR_CACHE, "a token cache call met a page number, a length or row offsets out of "
+                                         "range; what they name was skipped");
         if (v & 0x100u)
             return fail(FLARE_ERR_DEVICE_CHECK, "a device-side check failed (check %u); the access was skipped",
                         v & 0xffu);

@@ -121,6 +121,14 @@ flare_status_t encoder_fwd_with_workspace(const flare_dims_t *dims, const void *
                                           void *ws, size_t ws_bytes, cudaStream_t st);
 flare_status_t report_error(flare_status_t s, const char *msg);
 
+// Shared with the token cache's entry points (cache_api.cu): the current
+// device's multiprocessors and status word, the multiprocessor count that
+// planning uses (with or without a device), and the local decode.
+flare_status_t device_facts(int *sms, unsigned **status);
+int planning_multiprocessors();
+flare_status_t decode_with(const flare_dims_t *dims, const void *Q, const float *Z, const void *K, void *Y,
+                           cudaStream_t st, bool check_only);
+
 // Counts kernel launches for flare_launch_count (call once per <<<...>>>).
 void note_launch();
 

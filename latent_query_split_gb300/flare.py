@@ -12,7 +12,7 @@ from __future__ import annotations
 
 import ctypes
 import os
-from typing import Optional, Sequence
+from typing import NamedTuple, Optional, Sequence
 
 import torch
 
@@ -20,7 +20,7 @@ from . import build as _build
 
 FLARE_OK, FLARE_ERR_INVALID_ARG, FLARE_ERR_UNSUPPORTED = 0, 1, 2
 FLARE_ERR_WORKSPACE, FLARE_ERR_CUDA, FLARE_ERR_TIMEOUT = 3, 4, 5
-FLARE_ERR_DEVICE_CHECK = 6
+FLARE_ERR_DEVICE_CHECK, FLARE_ERR_CACHE = 6, 7
 FLARE_F32, FLARE_BF16 = 0, 1
 KERNELS = {"auto": 0, "simt": 1, "tensor": 2}
 (FLARE_OP_ENCODER_FWD, FLARE_OP_LSE_MERGE, FLARE_OP_DECODE_FWD, FLARE_OP_FWD,
@@ -33,6 +33,8 @@ EXPORTS = ("flare_workspace_bytes", "flare_encoder_fwd", "flare_lse_merge", "fla
            "flare_fwd", "flare_pp_fwd", "flare_encoder_bwd", "flare_decode_bwd",
            "flare_bwd", "flare_pp_bwd", "flare_encoder_fwd_noalloc",
            "flare_encoder_bwd_accumulate", "flare_check_bounded_wait",
+           "flare_cache_append", "flare_cache_workspace_bytes", "flare_cache_attn",
+           "flare_cache_encoder_fwd", "flare_cache_fwd",
            "flare_device_status", "flare_last_error_string", "flare_version",
            "flare_launch_count")
 
@@ -48,6 +50,19 @@ class FlareDims(ctypes.Structure):
                 ("N", ctypes.c_int), ("D", ctypes.c_int), ("scale", ctypes.c_float),
                 ("dtype", ctypes.c_int), ("q_batch_stride", ctypes.c_int64),
                 ("kernel", ctypes.c_int)]
+
+
+class FlareCacheDims(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int), ("H", ctypes.c_int), ("Hq", ctypes.c_int),
+                ("D", ctypes.c_int), ("page", ctypes.c_int), ("W", ctypes.c_int),
+                ("P", ctypes.c_int64), ("scale", ctypes.c_float), ("dtype", ctypes.c_int),
+                ("kernel", ctypes.c_int)]
+
+
+class FlareCachePtrs(ctypes.Structure):
+    """flare_cache_t: the device pointers of a FlareCache."""
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("page_table", ctypes.c_void_p)]
 
 
 _lib = None
@@ -90,6 +105,13 @@ def load_library(build_if_missing: bool = True):
     lib.flare_pp_bwd.argtypes = [D, P, P, P, P, P, P, P, I, P, P, P, P, P, P, P, P, P, P, P, P, Z, P]
     lib.flare_encoder_fwd_noalloc.argtypes = [D, P, P, P, P, P, I, P, P, P, P, P]
     lib.flare_check_bounded_wait.argtypes = [ctypes.c_uint, P]
+    C, CP, L64 = ctypes.POINTER(FlareCacheDims), ctypes.POINTER(FlareCachePtrs), ctypes.c_int64
+    lib.flare_cache_append.argtypes = [C, CP, P, P, L64, L64, L64, P, P, P, L64, P, P, I, I, P, P]
+    lib.flare_cache_workspace_bytes.argtypes = [C, L64]
+    lib.flare_cache_workspace_bytes.restype = Z
+    lib.flare_cache_attn.argtypes = [C, CP, P, L64, L64, P, P, I, P, P, P, Z, P]
+    lib.flare_cache_encoder_fwd.argtypes = [C, CP, I, P, L64, P, P, P, P, Z, P]
+    lib.flare_cache_fwd.argtypes = [C, CP, I, I, P, L64, P, P, P, P, P, P, P, P, Z, P]
     lib.flare_device_status.argtypes = [P]
     lib.flare_last_error_string.restype = ctypes.c_char_p
     lib.flare_version.restype = I
@@ -386,6 +408,227 @@ def flare_encoder_fwd_noalloc(Q, K, V, mask=None, shard_offsets=None, *, O_r=Non
                                          arr, R, _ptr(O_r), _ptr(L_r), _ptr(Z), _ptr(L),
                                          _stream(stream)))
     return O_r, L_r, Z, L
+
+
+# ---- paged 8-bit token cache ---------------------------------------------------
+class FlareCache(NamedTuple):
+    """Keys and values of B sequences as e4m3 codes in pages, one scale for each
+    page and head (see include/flare.h). k, v: float8_e4m3fn [P, H, page, D];
+    k_scale, v_scale: float32 [P, H]; page_table: int32 [B, W]."""
+    k: torch.Tensor
+    v: torch.Tensor
+    k_scale: torch.Tensor
+    v_scale: torch.Tensor
+    page_table: torch.Tensor
+
+
+def flare_cache_alloc(num_pages: int, H: int, D: int, page: int = 64, *, page_table, device="cuda"):
+    """A FlareCache of num_pages pages with the given page table (its slots are
+    not initialised: a slot is written before it is read)."""
+    codes = (num_pages, H, page, D)
+    k, v = (torch.empty(codes, dtype=torch.uint8, device=device).view(torch.float8_e4m3fn) for _ in range(2))
+    ks, vs = (torch.empty(codes[:2], dtype=torch.float32, device=device) for _ in range(2))
+    return FlareCache(k, v, ks, vs, page_table)
+
+
+_TOKEN_DTYPES = {torch.float32: FLARE_F32, torch.bfloat16: FLARE_BF16}
+
+
+def _cache_ptrs(cache: FlareCache):
+    k, v, ks, vs, table = cache
+    if k.dtype != torch.float8_e4m3fn or v.dtype != torch.float8_e4m3fn:
+        raise TypeError("a cache's codes are float8_e4m3fn")
+    if ks.dtype != torch.float32 or vs.dtype != torch.float32 or table.dtype != torch.int32:
+        raise TypeError("a cache's scales are float32 and its page table is int32")
+    if k.dim() != 4 or table.dim() != 2 or v.shape != k.shape or ks.shape != k.shape[:2] or vs.shape != ks.shape:
+        raise ValueError("cache shapes do not match: k, v [P, H, page, D], scales [P, H], page_table [B, W]")
+    dev = k.device
+    if v.device != dev or ks.device != dev or vs.device != dev or table.device != dev:
+        raise ValueError("the cache's tensors are on different devices")
+    return FlareCachePtrs(_ptr(k), _ptr(v), _ptr(ks), _ptr(vs), _ptr(table))
+
+
+def _cache_dims(cache: FlareCache, Hq: int, dtype, scale=None, kernel="auto"):
+    P, H, page, D = cache.k.shape
+    if dtype not in _TOKEN_DTYPES:
+        raise TypeError(f"unsupported token dtype {dtype}")
+    if cache.k.device.index != torch.cuda.current_device():
+        raise ValueError("the cache is not on the current device")
+    B, W = cache.page_table.shape
+    return FlareCacheDims(B, H, Hq, D, page, W, P, 0.0 if scale is None else float(scale),
+                          _TOKEN_DTYPES[dtype], KERNELS[kernel])
+
+
+def _like(t, what, dtype, shape, device):
+    """Pointer of an optional tensor after checks of its type, shape and device."""
+    if t is None:
+        return None
+    if t.dtype != dtype or tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{what} must be {dtype} of shape {tuple(shape)}")
+    if t.device != device:
+        raise ValueError(f"{what} is on another device than the cache")
+    return _ptr(t)
+
+
+def _rows(x, what, heads, D, B, cu, dtype, device):
+    """(pointer, token stride, T) of token rows [B, n, heads, D] or, with
+    cu_seqlens, [T, heads, D]; a token's channels are contiguous, the tokens
+    evenly spaced."""
+    if x.dtype != dtype:
+        raise TypeError(f"{what} must be {dtype}")
+    if x.dim() != (4 if cu is None else 3) or x.shape[-2:] != (heads, D) or (cu is None and x.shape[0] != B):
+        raise ValueError(f"{what} must be [B, n, {heads}, {D}], or [T, {heads}, {D}] with cu_seqlens")
+    if x.device != device:
+        raise ValueError(f"{what} is on another device than the cache")
+    T = x.shape[0] * x.shape[1] if cu is None else x.shape[0]
+    if x.is_contiguous():
+        return x.data_ptr(), 0, T
+    st = x.stride()
+    even = cu is not None or x.shape[0] == 1 or x.shape[1] == 1 or st[0] == x.shape[1] * st[1]
+    if st[-1] != 1 or (heads > 1 and st[-2] != D) or not even:
+        raise ValueError(f"{what}: a token's channels must be contiguous and the tokens evenly spaced")
+    step = st[0] if cu is not None or x.shape[1] == 1 else st[1]
+    if T > 1 and step < heads * D:
+        raise ValueError(f"{what}: tokens overlap")
+    return x.data_ptr(), (step if T > 1 else 0), T
+
+
+def flare_cache_append(cache: FlareCache, K, V, seq_lens, *, cu_seqlens=None, Q=None, inv_freq=None,
+                       interleaved=False, Q_out=None, seq_lens_out=None, stream=None):
+    """New tokens K, V ([B,n,H,D], or [T,H,D] with int32 cu_seqlens [B+1]) enter
+    the cache behind the seq_lens tokens that each sequence holds; with inv_freq
+    (fp32 [rot/2]) keys and the queries Q are rotated by their positions.
+    Returns (seq_lens_out, Q_out)."""
+    lib = load_library()
+    ptrs = _cache_ptrs(cache)
+    dev = cache.k.device
+    B, H, D = cache.page_table.shape[0], cache.k.shape[1], cache.k.shape[3]
+    dims = _cache_dims(cache, 0 if Q is None else Q.shape[-2], K.dtype)
+    k, k_st, T = _rows(K, "K", H, D, B, cu_seqlens, K.dtype, dev)
+    v, v_st, Tv = _rows(V, "V", H, D, B, cu_seqlens, K.dtype, dev)
+    q, q_st, Tq = (None, 0, T) if Q is None else _rows(Q, "Q", dims.Hq, D, B, cu_seqlens, K.dtype, dev)
+    if Tv != T or Tq != T:
+        raise ValueError("K, V and Q have different numbers of tokens")
+    if Q is not None and Q_out is None:
+        Q_out = torch.empty(Q.shape, dtype=Q.dtype, device=dev)
+    if seq_lens_out is None:
+        seq_lens_out = torch.empty_like(seq_lens)
+    if inv_freq is not None and (inv_freq.dim() != 1 or inv_freq.shape[0] < 1):
+        raise ValueError("inv_freq must be [rot / 2]")
+    rot = 0 if inv_freq is None else 2 * inv_freq.shape[0]
+    _check(lib.flare_cache_append(
+        ctypes.byref(dims), ctypes.byref(ptrs), k, v, k_st, v_st, T,
+        _like(seq_lens, "seq_lens", torch.int32, (B,), dev),
+        _like(cu_seqlens, "cu_seqlens", torch.int32, (B + 1,), dev), q, q_st,
+        None if Q is None else _like(Q_out, "Q_out", K.dtype, Q.shape, dev),
+        _like(inv_freq, "inv_freq", torch.float32, (rot // 2,), dev), rot, int(interleaved),
+        _like(seq_lens_out, "seq_lens_out", torch.int32, (B,), dev), _stream(stream)))
+    return seq_lens_out, Q_out
+
+
+def flare_cache_workspace_bytes(dims: FlareCacheDims, T: int) -> int:
+    n = load_library().flare_cache_workspace_bytes(ctypes.byref(dims), T)
+    if n == ctypes.c_size_t(-1).value:
+        _check(FLARE_ERR_INVALID_ARG)
+    return int(n)
+
+
+def _cache_workspace(dims, T, workspace, device):
+    if workspace is None:
+        workspace = torch.empty(max(flare_cache_workspace_bytes(dims, T), 1), dtype=torch.uint8, device=device)
+    elif workspace.device != device:
+        raise ValueError("workspace is on another device than the cache")
+    return _ptr(workspace), workspace.numel() * workspace.element_size()
+
+
+def flare_cache_attn(Q, cache: FlareCache, seq_lens, *, cu_seqlens=None, causal=True, O=None, L=None,
+                     workspace=None, scale=None, kernel="auto", stream=None):
+    """Attention of Q ([B,n,Hq,D], or [T,Hq,D] with int32 cu_seqlens [B+1]) over
+    the seq_lens tokens that the cache holds for each sequence; returns (O, L):
+    O like Q, L fp32 without the channels."""
+    lib = load_library()
+    ptrs = _cache_ptrs(cache)
+    dev = cache.k.device
+    B, D = cache.page_table.shape[0], cache.k.shape[3]
+    dims = _cache_dims(cache, Q.shape[-2], Q.dtype, scale, kernel)
+    q, q_st, T = _rows(Q, "Q", dims.Hq, D, B, cu_seqlens, Q.dtype, dev)
+    if O is None:
+        O = torch.empty(Q.shape, dtype=Q.dtype, device=dev)
+    if L is None:
+        L = torch.empty(Q.shape[:-1], dtype=torch.float32, device=dev)
+    ws, nbytes = _cache_workspace(dims, T, workspace, dev)
+    _check(lib.flare_cache_attn(
+        ctypes.byref(dims), ctypes.byref(ptrs), q, q_st, T,
+        _like(seq_lens, "seq_lens", torch.int32, (B,), dev),
+        _like(cu_seqlens, "cu_seqlens", torch.int32, (B + 1,), dev), int(causal),
+        _like(O, "O", Q.dtype, Q.shape, dev), _like(L, "L", torch.float32, Q.shape[:-1], dev), ws, nbytes,
+        _stream(stream)))
+    return O, L
+
+
+def _latents(Q, cache):
+    """(M, q_batch_stride) of latent queries [H,M,D] or [B,H,M,D]."""
+    B, H, D = cache.page_table.shape[0], cache.k.shape[1], cache.k.shape[3]
+    M = Q.shape[-2]
+    if tuple(Q.shape) not in ((H, M, D), (B, H, M, D)) or Q.device != cache.k.device:
+        raise ValueError("Q must be [H, M, D] or [B, H, M, D] on the cache's device")
+    return M, (0 if Q.dim() == 3 else H * M * D)
+
+
+def flare_cache_encoder_fwd(Q, cache: FlareCache, seq_lens, *, Z=None, L=None, workspace=None, scale=None,
+                            kernel="auto", stream=None):
+    """The FLARE encoder over the cached tokens: latent queries Q ([H,M,D] or
+    [B,H,M,D]); returns (Z [B,H,M,D], L [B,H,M]) in fp32."""
+    lib = load_library()
+    ptrs = _cache_ptrs(cache)
+    dev = cache.k.device
+    B, H, D = cache.page_table.shape[0], cache.k.shape[1], cache.k.shape[3]
+    M, qbs = _latents(Q, cache)
+    dims = _cache_dims(cache, H, Q.dtype, scale, kernel)
+    f32 = dict(dtype=torch.float32, device=dev)
+    if Z is None:
+        Z = torch.empty((B, H, M, D), **f32)
+    if L is None:
+        L = torch.empty((B, H, M), **f32)
+    ws, nbytes = _cache_workspace(dims, B * M, workspace, dev)
+    _check(lib.flare_cache_encoder_fwd(
+        ctypes.byref(dims), ctypes.byref(ptrs), M, _ptr(Q), qbs,
+        _like(seq_lens, "seq_lens", torch.int32, (B,), dev), _like(Z, "Z", torch.float32, (B, H, M, D), dev),
+        _like(L, "L", torch.float32, (B, H, M), dev), ws, nbytes, _stream(stream)))
+    return Z, L
+
+
+def flare_cache_fwd(Q, cache: FlareCache, K, V, seq_lens, *, seq_lens_out=None, Y=None, Z=None, L=None,
+                    workspace=None, scale=None, kernel="auto", stream=None):
+    """FLARE mixer forward over a growing token set: K, V [B,N,H,D] enter the
+    cache, the latents Q gather Z from all the tokens held, the new tokens decode
+    against them; returns (Y [B,N,H,D], Z, L, seq_lens_out)."""
+    lib = load_library()
+    ptrs = _cache_ptrs(cache)
+    dev = cache.k.device
+    B, H, D = cache.page_table.shape[0], cache.k.shape[1], cache.k.shape[3]
+    M, qbs = _latents(Q, cache)
+    dims = _cache_dims(cache, H, Q.dtype, scale, kernel)
+    if K.dim() != 4:
+        raise ValueError("K must be [B, N, H, D]")
+    N = K.shape[1]
+    shape, f32 = (B, N, H, D), dict(dtype=torch.float32, device=dev)
+    if Y is None:
+        Y = torch.empty(shape, dtype=Q.dtype, device=dev)
+    if Z is None:
+        Z = torch.empty((B, H, M, D), **f32)
+    if L is None:
+        L = torch.empty((B, H, M), **f32)
+    if seq_lens_out is None:
+        seq_lens_out = torch.empty_like(seq_lens)
+    ws, nbytes = _cache_workspace(dims, B * M, workspace, dev)
+    _check(lib.flare_cache_fwd(
+        ctypes.byref(dims), ctypes.byref(ptrs), M, N, _ptr(Q), qbs, _like(K, "K", Q.dtype, shape, dev),
+        _like(V, "V", Q.dtype, shape, dev), _like(seq_lens, "seq_lens", torch.int32, (B,), dev),
+        _like(seq_lens_out, "seq_lens_out", torch.int32, (B,), dev), _like(Y, "Y", Q.dtype, shape, dev),
+        _like(Z, "Z", torch.float32, (B, H, M, D), dev), _like(L, "L", torch.float32, (B, H, M), dev), ws,
+        nbytes, _stream(stream)))
+    return Y, Z, L, seq_lens_out
 
 
 def flare_check_bounded_wait(limit_us: int, stream=None):
