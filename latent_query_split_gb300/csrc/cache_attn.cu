@@ -225,9 +225,10 @@ __global__ void __launch_bounds__(128) attn_merge_kernel(const AttnArgs a, const
 // ---- choice and launch ----------------------------------------------------------------
 AttnPlan attn_plan(const Pool &c, int G, bool bf16, int64_t T, int family, int sms) {
     AttnPlan p;
-    p.kernel = AttnKernel::kSimt;
-    p.rows = 8;
-    int64_t grid = (int64_t)sms * 4;
+    p.kernel = family == FLARE_KERNEL_SIMT ? AttnKernel::kSimt : AttnKernel::kMma;
+    const int64_t per_seq = c.B > 0 ? T * G / c.B : 0;      // rows of a head and sequence on average
+    p.rows = p.kernel == AttnKernel::kSimt ? 8 : bf16 && per_seq > 16 ? 32 : 16;
+    int64_t grid = (int64_t)sms * (p.kernel == AttnKernel::kSimt ? 4 : 1);
     // no more spans than there can be tiles
     const int64_t tiles = ((T * G + p.rows - 1) / p.rows + c.B) * c.H *
                           (((int64_t)c.W * c.page + kTile - 1) / kTile + 1);
@@ -260,13 +261,17 @@ cudaError_t launch_pdl(Kernel k, dim3 grid, dim3 block, cudaStream_t st, Args...
 }  // namespace
 
 cudaError_t launch_attn(const AttnArgs &a, AttnKernel kernel, bool bf16, cudaStream_t st) {
-    (void)kernel;
-    if (bf16)
-        attn_simt_kernel<8, true><<<a.grid, 128, 0, st>>>(a);
-    else
-        attn_simt_kernel<8, false><<<a.grid, 128, 0, st>>>(a);
-    note_launch();
-    cudaError_t e = cudaGetLastError();
+    cudaError_t e;
+    if (kernel == AttnKernel::kSimt) {
+        if (bf16)
+            attn_simt_kernel<8, true><<<a.grid, 128, 0, st>>>(a);
+        else
+            attn_simt_kernel<8, false><<<a.grid, 128, 0, st>>>(a);
+        note_launch();
+        e = cudaGetLastError();
+    } else {
+        e = launch_attn_mma(a, bf16, st);
+    }
     if (e != cudaSuccess) return e;
     e = launch_pdl(attn_merge_kernel, dim3(a.grid, (a.rows + 3) / 4), dim3(128), st, a,
                    (int)(!bf16 || a.o_f32));

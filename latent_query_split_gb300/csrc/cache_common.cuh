@@ -69,6 +69,7 @@ struct AttnPlan {
 AttnPlan attn_plan(const Pool &c, int G, bool bf16, int64_t T, int family, int sms);
 
 cudaError_t launch_attn(const AttnArgs &a, AttnKernel kernel, bool bf16, cudaStream_t st);
+cudaError_t launch_attn_mma(const AttnArgs &a, bool bf16, cudaStream_t st);
 cudaError_t launch_append(const AppendArgs &a, bool bf16, cudaStream_t st);
 
 }  // namespace cache
