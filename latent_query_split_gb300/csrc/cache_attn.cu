@@ -227,7 +227,10 @@ AttnPlan attn_plan(const Pool &c, int G, bool bf16, int64_t T, int family, int s
     AttnPlan p;
     p.kernel = family == FLARE_KERNEL_SIMT ? AttnKernel::kSimt : AttnKernel::kMma;
     const int64_t per_seq = c.B > 0 ? T * G / c.B : 0;      // rows of a head and sequence on average
-    p.rows = p.kernel == AttnKernel::kSimt ? 8 : bf16 && per_seq > 16 ? 32 : 16;
+    if (p.kernel == AttnKernel::kMma && bf16 && (c.D == 64 || c.D == 128) && per_seq > 32) p.kernel = AttnKernel::kTc;
+    p.rows = p.kernel == AttnKernel::kSimt ? 8 : p.kernel == AttnKernel::kTc ? (per_seq > 128 ? 256 : 128)
+             : bf16 && per_seq > 16        ? 32
+                                           : 16;
     int64_t grid = (int64_t)sms * (p.kernel == AttnKernel::kSimt ? 4 : 1);
     // no more spans than there can be tiles
     const int64_t tiles = ((T * G + p.rows - 1) / p.rows + c.B) * c.H *
@@ -269,6 +272,8 @@ cudaError_t launch_attn(const AttnArgs &a, AttnKernel kernel, bool bf16, cudaStr
             attn_simt_kernel<8, false><<<a.grid, 128, 0, st>>>(a);
         note_launch();
         e = cudaGetLastError();
+    } else if (kernel == AttnKernel::kTc) {
+        e = launch_attn_tc(a, st);
     } else {
         e = launch_attn_mma(a, bf16, st);
     }

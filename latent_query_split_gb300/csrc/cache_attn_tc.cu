@@ -1,0 +1,714 @@
+// cache_attn_tc.cu -- attention over the paged 8-bit cache for many query rows
+// a shared head (prompts, latents): tcgen05, TMEM and TMA. bf16 queries, D = 64
+// or 128.
+//
+// Per item (sequence, row tile of 128 * RT rows, head) and tile of 128 tokens:
+//   S = Q K^T   kind::f8f6f4: K is used as the cache holds it, its pages' codes
+//               fetched by TMA into swizzled rows. A query row, scaled by a power
+//               of two so that its largest channel lies in [2^7, 2^8), is the sum
+//               of an e4m3 part (its upper 4 bits) and an e5m2 part (the other 4;
+//               5 bits of exponent reach where e4m3's 4 do not): exact for
+//               channels within 2^-14 of the row's largest, off by 2^-21 of that
+//               for smaller ones. Two 8-bit products take as long as one of 16
+//               bits, and K is neither converted nor written a second time.
+//   w = 2^(S factor ks + ev - m)  one row a thread; ks = the page's key scale, 2^ev
+//               its value scale, m a reference at most 15 below the row's
+//               largest exponent, moved (with O and l) only when that is passed.
+//   O += w V    kind::f16: w in fp16 from TMEM (in place of S), V converted to
+//               fp16 (exact) by four warps into MN-major tiles. Rows of V that no
+//               token stands behind are written as zeros there: a cache's unused
+//               slots may hold NaN codes, and 0 * NaN is not 0.
+//   l += 2^-ev sum w.
+//
+// Roles (16 warps): 0 fetches pages and scales, 1 issues O += w V, 2 issues S,
+// 3 is idle, 4-7 stage Q and convert V, 8-11 and 12-15 are two softmax groups.
+// RT = 2: group g has rows 128 g ..; RT = 1: the groups take tiles in turn, each
+// with an accumulator of its own, joined at the end of the item. Unit q = (tile,
+// group) in order; its S lies in TMEM buffer q % NB, of which 512 columns hold
+// two beside two 128-channel accumulators and three beside 64-channel ones. So
+// one group's products run under the other's exponentials.
+#include "cache_device.cuh"
+#include "tc_host.cuh"
+
+namespace flare {
+namespace cache {
+namespace {
+
+using namespace tc;
+
+constexpr float kNoMax = -3.0e38f;
+constexpr float kHeadroom = 15.f;        // w <= 2^15: fp16 holds 65504
+constexpr float kFresh = 7.f;            // a new largest score starts at w = 2^7
+
+template <int D_, int RT_>
+struct TcCfg {
+    static constexpr int D = D_, RT = RT_;
+    static constexpr int ROWS = 128 * RT;
+    static constexpr int THREADS = 512;
+    static constexpr int NB = D == 128 ? 2 : 3;                        // S buffers
+    static constexpr int KSTG = D == 128 ? (RT == 2 ? 3 : 4) : 6;      // key stages
+    static constexpr int VSTG = D == 128 ? (RT == 2 ? 2 : 3) : 6;      // value stages (codes)
+    // a tile's scales outlive its stages by the units between S and O
+    static constexpr int NSC = 16;
+    static_assert(NSC >= KSTG + NB + 1, "scale ring too short");
+    static constexpr uint32_t O_COL = NB * 128;
+    static_assert(O_COL + 2 * D <= 512, "tensor-memory columns exceeded");
+    static constexpr uint32_t TILE8 = 128 * D;                         // a tile of codes
+    static constexpr uint32_t TILE16 = 2 * TILE8;
+    static constexpr uint32_t Q_OFF = 0;                               // per row tile: e4m3 part, e5m2 part
+    static constexpr uint32_t K_OFF = Q_OFF + RT * 2 * TILE8;
+    static constexpr uint32_t V8_OFF = K_OFF + KSTG * TILE8;
+    static constexpr uint32_t V16_OFF = V8_OFF + VSTG * TILE8;
+    static constexpr uint32_t SC_OFF = V16_OFF + 2 * TILE16;           // [NSC][8] {ks, ev, 1 / vs, valid}
+    static constexpr uint32_t FAC_OFF = SC_OFF + NSC * 8 * 16;         // [ROWS] row factors
+    static constexpr uint32_t STAT_OFF = FAC_OFF + ROWS * 4;           // RT = 1: [2][128] (m, l)
+    static constexpr uint32_t BAR_OFF = STAT_OFF + (RT == 1 ? 2048 : 0);
+    static constexpr int NBAR = 2 * KSTG + 2 * VSTG + NSC + 4 + 2 + 3 * NB + 2 + 3;
+    static constexpr uint32_t MISC_OFF = BAR_OFF + NBAR * 8;
+    static constexpr uint32_t BYTES = MISC_OFF + 16;
+    static constexpr uint32_t ALLOC = BYTES + 1024;
+    static_assert(ALLOC <= 232448, "shared memory budget of one CTA exceeded");
+    // registers per thread of each warpgroup: 128 at launch, 72 + 72 + 184 + 184 = 4 x 128
+    static constexpr uint32_t REG_CTL = 72, REG_CVT = 72, REG_SOFT = 184;
+};
+
+template <uint32_t R>
+__device__ __forceinline__ void regs_inc() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R));
+}
+template <uint32_t R>
+__device__ __forceinline__ void regs_dec() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R));
+}
+
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+__device__ __forceinline__ uint32_t pack_e4m3(float lo, float hi) {
+    uint16_t r;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+__device__ __forceinline__ uint32_t pack_e5m2(float lo, float hi) {
+    uint16_t r;
+    asm("cvt.rn.satfinite.e5m2x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+__device__ __forceinline__ uint4 lds16(uint32_t a) {
+    uint4 v;
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
+    return v;
+}
+__device__ __forceinline__ void sts16(uint32_t a, uint4 v) {
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+
+// The pieces of a CTA's span, in order: what every role walks.
+struct Piece {
+    Cursor cur;
+    int k0, k1;                          // tiles [k0, k1) of the item
+    __device__ __forceinline__ bool begin(const Cursor &c) {
+        cur = c;
+        return set();
+    }
+    __device__ __forceinline__ bool set() {
+        if (cur.tiles_left <= 0) return false;
+        k0 = cur.k;
+        k1 = imin(cur.nt, cur.k + cur.tiles_left);
+        return true;
+    }
+    __device__ __forceinline__ bool next(const AttnArgs &a) {
+        cur.tiles_left -= k1 - k0;
+        if (cur.tiles_left <= 0) return false;
+        next_item(a, cur);
+        return set();
+    }
+};
+
+template <int D, int RT>
+__global__ void __launch_bounds__(512, 1)
+attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const AttnArgs a) {
+    using C = TcCfg<D, RT>;
+    constexpr int NB = C::NB, KSTG = C::KSTG, VSTG = C::VSTG, NSC = C::NSC;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    __shared__ int64_t scan_sh[16];
+    __shared__ Cursor cur_sh;
+    const uint32_t sbase = smem_u32(smem);
+    const uint32_t bar0 = sbase + C::BAR_OFF;
+    int nbar = 0;
+    auto bars = [&](int n) {
+        const uint32_t b = bar0 + 8u * nbar;
+        nbar += n;
+        return b;
+    };
+    const uint32_t k_full = bars(KSTG), k_empty = bars(KSTG), v_full = bars(VSTG), v_empty = bars(VSTG), sc_full = bars(NSC),
+                   h_full = bars(2), h_empty = bars(2), q_full = bars(1), q_read = bars(1), s_full = bars(NB),
+                   p_full = bars(NB), buf_free = bars(NB), o_done = bars(2), soft = bars(1), drain = bars(2);
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::MISC_OFF);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + C::MISC_OFF + 4);
+    const float4 *const sc_sh = reinterpret_cast<const float4 *>(smem + C::SC_OFF);
+    float *const factor = reinterpret_cast<float *>(smem + C::FAC_OFF);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, cta = blockIdx.x;
+    Waiter wt{abort_flag, a.status};
+    auto wwait = [&](uint32_t bar, uint32_t par) -> bool { return __all_sync(0xffffffffu, wt.wait_inline(bar, par)); };
+
+    if (threadIdx.x == 0) {
+        *abort_flag = 0;
+        for (int s = 0; s < KSTG; ++s) {
+            mbar_init(k_full + 8 * s, 1);
+            mbar_init(k_empty + 8 * s, 1);
+        }
+        for (int s = 0; s < VSTG; ++s) {
+            mbar_init(v_full + 8 * s, 1);
+            mbar_init(v_empty + 8 * s, 4);           // the converting warps
+        }
+        for (int s = 0; s < NSC; ++s) mbar_init(sc_full + 8 * s, 1);
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(h_full + 8 * s, 4);
+            mbar_init(h_empty + 8 * s, 1);
+            mbar_init(o_done + 8 * s, 1);
+            mbar_init(drain + 8 * s, 1);
+        }
+        mbar_init(q_full, 4);
+        mbar_init(q_read, 8);                        // the softmax warps
+        for (int b = 0; b < NB; ++b) {
+            mbar_init(s_full + 8 * b, 1);
+            mbar_init(p_full + 8 * b, 4);            // the owning group's warps
+            mbar_init(buf_free + 8 * b, 1);
+        }
+        mbar_init(soft, 8);
+        fence_mbar_init();
+    }
+    if (warp == 0 && lane == 0) {
+        prefetch_tmap(&tmK);
+        prefetch_tmap(&tmV);
+    }
+    if (warp == 1) {
+        tmem_alloc(smem_u32(tmem_slot), 512);
+        tmem_relinquish();
+    }
+    const Span sp = find_span<512>(a, cta, scan_sh, &cur_sh);
+    const Cursor cur0 = cur_sh;
+    if (threadIdx.x == 0) write_record(a, sp, cur0, cta);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    Piece pc;
+
+    if (warp < 4) {
+        regs_dec<C::REG_CTL>();
+        if (warp == 0) {
+            // ---------------- pages and scales ----------------
+            // Lane i holds group i (16 tokens) of four tiles at a time; page numbers are
+            // read two batches ahead, scales one.
+            int j = 0;
+            bool ok = true;
+            for (bool more = pc.begin(cur0); more && ok; more = pc.next(a)) {
+                const int seen = visible(pc.cur.s, a.G, a.rows, pc.cur.rt, a.causal);
+                const int32_t *const row_table = a.c.table + (int64_t)pc.cur.b * a.c.W;
+                const int nb = (pc.k1 - pc.k0 + 3) >> 2;
+                auto page_of_batch = [&](int batch) -> int {
+                    const int k = pc.k0 + 4 * batch + (lane >> 3), n = k * kTile + 16 * (lane & 7);
+                    return k < pc.k1 && n < seen ? row_table[n >> a.c.page_log2] : -2;
+                };
+                auto checked = [&](int p) -> int {
+                    if (p == -2) return -1;
+                    if (p < 0 || p >= a.c.P) {
+                        flag_bad(a.status);
+                        return -1;
+                    }
+                    return p;
+                };
+                int page = checked(page_of_batch(0)), page1 = nb > 1 ? page_of_batch(1) : -2;
+                float ks = 0.f, vs = 0.f;
+                auto scales = [&](int p, float &x, float &y) {
+                    x = y = 0.f;
+                    if (p >= 0) {
+                        x = a.c.ks[(int64_t)p * a.c.H + pc.cur.h];
+                        y = a.c.vs[(int64_t)p * a.c.H + pc.cur.h];
+                    }
+                };
+                scales(page, ks, vs);
+                for (int batch = 0; batch < nb && ok; ++batch) {
+                    const int npage = checked(page1);
+                    float nks, nvs;
+                    scales(npage, nks, nvs);
+                    page1 = page_of_batch(batch + 2);
+                    for (int sub = 0; sub < 4 && ok; ++sub) {
+                        const int k = pc.k0 + 4 * batch + sub;
+                        if (k >= pc.k1) break;
+                        const int ksl = j % KSTG, vsl = j % VSTG, scl = j % NSC;
+                        const bool mine = (lane >> 3) == sub;
+                        const int grp = lane & 7;
+                        const bool load = mine && page >= 0 && ((grp * 16) & (a.c.page - 1)) == 0;
+                        const int count = __popc(__ballot_sync(0xffffffffu, load));
+                        const uint32_t bytes = (uint32_t)a.c.page * D;
+                        const int row = load ? (page * a.c.H + pc.cur.h) << a.c.page_log2 : 0;
+                        if (!(ok = wwait(k_empty + 8 * ksl, ((uint32_t)(j / KSTG) & 1) ^ 1))) break;
+                        if (mine) {
+                            const int ex = (int)((__float_as_uint(vs) >> 23) & 0xff);
+                            *reinterpret_cast<float4 *>(smem + C::SC_OFF + (scl * 8 + grp) * 16) =
+                                page >= 0 ? make_float4(ks, (float)(ex - 127), __int_as_float((254 - ex) << 23), 1.f)
+                                          : make_float4(0.f, 0.f, 0.f, 0.f);
+                        }
+                        __syncwarp();
+                        if (lane == 0) {
+                            mbar_arrive(sc_full + 8 * scl);
+                            mbar_arrive_expect_tx(k_full + 8 * ksl, count * bytes);
+                        }
+                        __syncwarp();
+                        if (load) tma_load_2d(sbase + C::K_OFF + ksl * C::TILE8 + grp * 16 * D, &tmK, 0, row, k_full + 8 * ksl);
+                        __syncwarp();
+                        if (!(ok = wwait(v_empty + 8 * vsl, ((uint32_t)(j / VSTG) & 1) ^ 1))) {
+                            ++j;
+                            break;
+                        }
+                        if (lane == 0) mbar_arrive_expect_tx(v_full + 8 * vsl, count * bytes);
+                        __syncwarp();
+                        if (load) tma_load_2d(sbase + C::V8_OFF + vsl * C::TILE8 + grp * 16 * D, &tmV, 0, row, v_full + 8 * vsl);
+                        __syncwarp();
+                        ++j;
+                    }
+                    page = npage;
+                    ks = nks;
+                    vs = nvs;
+                }
+            }
+            if (wt.aborted() && lane == 0) {
+                // every issued copy lands before the CTA goes
+                const uint64_t t0 = globaltimer();
+                for (int x = j > KSTG ? j - KSTG : 0; x < j; ++x)
+                    while (!mbar_try_wait(k_full + 8 * (x % KSTG), (uint32_t)(x / KSTG) & 1) && globaltimer() - t0 < 500000000ull) {
+                    }
+                for (int x = j > VSTG ? j - VSTG : 0; x < j; ++x)
+                    while (!mbar_try_wait(v_full + 8 * (x % VSTG), (uint32_t)(x / VSTG) & 1) && globaltimer() - t0 < 500000000ull) {
+                    }
+            }
+        } else if (warp == 2) {
+            // ---------------- S = Q K^T ----------------
+            constexpr uint32_t idHi = idesc_f8(128, 128, 0), idLo = idesc_f8(128, 128, 1);
+            int j = 0, q = 0;
+            uint32_t pieces = 0;
+            bool ok = true;
+            auto desc = [&](uint32_t at) { return D == 128 ? desc_sw128(at, 16, 1024) : desc_sw64(at); };
+            for (bool more = pc.begin(cur0); more && ok; more = pc.next(a)) {
+                if (!(ok = wwait(q_full, pieces++ & 1))) break;
+                for (int k = pc.k0; k < pc.k1 && ok; ++k, ++j) {
+                    if (!(ok = wwait(k_full + 8 * (j % KSTG), (uint32_t)(j / KSTG) & 1))) break;
+                    const uint64_t dK = desc(sbase + C::K_OFF + (j % KSTG) * C::TILE8);
+#pragma unroll
+                    for (int g = 0; g < RT; ++g, ++q) {
+                        const int b = q % NB;
+                        if (q >= NB && !(ok = wwait(buf_free + 8 * b, (uint32_t)(q / NB - 1) & 1))) break;
+                        tc_fence_after();
+                        const uint64_t dHi = desc(sbase + C::Q_OFF + g * 2 * C::TILE8);
+                        const uint64_t dLo = desc(sbase + C::Q_OFF + (g * 2 + 1) * C::TILE8);
+#pragma unroll
+                        for (int kb = 0; kb < D / 32; ++kb) {
+                            umma_f8_ss_elect(tmem + b * 128, dHi + 2 * kb, dK + 2 * kb, idHi, kb > 0);
+                            umma_f8_ss_elect(tmem + b * 128, dLo + 2 * kb, dK + 2 * kb, idLo, 1u);
+                        }
+                        umma_commit_elect(s_full + 8 * b);
+                    }
+                    if (ok) umma_commit_elect(k_empty + 8 * (j % KSTG));
+                }
+            }
+            if (wt.aborted()) {
+                umma_commit_elect(drain);
+                const uint64_t t0 = globaltimer();
+                while (!mbar_try_wait(drain, 0) && globaltimer() - t0 < 500000000ull) {
+                }
+            }
+            __syncwarp();
+        } else if (warp == 1) {
+            // ---------------- O += w V ----------------
+            constexpr uint32_t idPV = idesc_f16(128, D, 0, 1);
+            int j = 0, q = 0;
+            bool ok = true;
+            for (bool more = pc.begin(cur0); more && ok; more = pc.next(a)) {
+                bool fresh[2] = {true, true};
+                for (int k = pc.k0; k < pc.k1 && ok; ++k, ++j) {
+                    const uint32_t vb = sbase + C::V16_OFF + (j & 1) * C::TILE16;
+                    const uint64_t dV = desc_sw128(vb, 128 * 128, 1024);
+#pragma unroll
+                    for (int u = 0; u < RT; ++u, ++q) {
+                        const int g = q & 1, b = q % NB;
+                        if (!(ok = wwait(p_full + 8 * b, (uint32_t)(q / NB) & 1))) break;
+                        if (u == 0 && !(ok = wwait(h_full + 8 * (j & 1), (uint32_t)(j >> 1) & 1))) break;
+                        tc_fence_after();
+#pragma unroll
+                        for (int kb = 0; kb < 8; ++kb)
+                            umma_ts_elect(tmem + C::O_COL + g * D, tmem + b * 128 + kb * 8, dV + (uint64_t)(kb * 16 * 128 >> 4),
+                                          idPV, kb > 0 || !fresh[g]);
+                        fresh[g] = false;
+                        umma_commit_elect(o_done + 8 * g);
+                        umma_commit_elect(buf_free + 8 * b);
+                    }
+                    if (ok) umma_commit_elect(h_empty + 8 * (j & 1));
+                }
+            }
+            if (wt.aborted()) {
+                umma_commit_elect(drain + 8);
+                const uint64_t t0 = globaltimer();
+                while (!mbar_try_wait(drain + 8, 0) && globaltimer() - t0 < 500000000ull) {
+                }
+            }
+            __syncwarp();
+        }
+    } else if (warp < 8) {
+        // ---------------- Q into two 8-bit parts; V into fp16 ----------------
+        regs_dec<C::REG_CVT>();
+        const int tid = threadIdx.x - 128;           // 0 .. 127
+        int j = 0, q = 0;
+        uint32_t pieces = 0;
+        bool ok = true;
+        for (bool more = pc.begin(cur0); more && ok; more = pc.next(a), ++pieces) {
+            if (pieces > 0) {
+                // the last piece's factors have been read and its S products are done
+                if (!(ok = wwait(q_read, (pieces - 1) & 1))) break;
+                if (!(ok = wwait(s_full + 8 * ((q - 1) % NB), (uint32_t)((q - 1) / NB) & 1))) break;
+            }
+#pragma unroll 1
+            for (int g = 0; g < RT; ++g) {
+                const RowPlace p = row_place(a, pc.cur.s, pc.cur.b, pc.cur.rt, pc.cur.h, g * 128 + tid);
+                const __nv_bfloat16 *src = reinterpret_cast<const __nv_bfloat16 *>(a.Q) + p.q;
+                const bool vec = (reinterpret_cast<uintptr_t>(src) & 15) == 0;
+                auto chunk = [&](int c, uint32_t (&x)[8]) {          // 16 channels, bf16 pairs
+                    if (!p.valid) {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) x[i] = 0u;
+                    } else if (vec) {
+                        const uint4 u = reinterpret_cast<const uint4 *>(src)[2 * c], v = reinterpret_cast<const uint4 *>(src)[2 * c + 1];
+                        x[0] = u.x; x[1] = u.y; x[2] = u.z; x[3] = u.w;
+                        x[4] = v.x; x[5] = v.y; x[6] = v.z; x[7] = v.w;
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const __nv_bfloat162 y = __halves2bfloat162(src[16 * c + 2 * i], src[16 * c + 2 * i + 1]);
+                            x[i] = *reinterpret_cast<const uint32_t *>(&y);
+                        }
+                    }
+                };
+                uint32_t top = 0;
+#pragma unroll 1
+                for (int c = 0; c < D / 16; ++c) {
+                    uint32_t x[8];
+                    chunk(c, x);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) top = max(top, max(x[i] & 0x7fff0000u, (x[i] & 0x7fffu) << 16));
+                }
+                const int e = imax((int)(top >> 23) - 127, -100);
+                const float inv = __int_as_float((7 - e + 127) << 23);
+                factor[g * 128 + tid] = top >= 0x7f800000u ? NAN : __int_as_float((e - 7 + 127) << 23) * a.sl2;
+                const uint32_t hi0 = sbase + C::Q_OFF + g * 2 * C::TILE8 + tid * D;
+#pragma unroll 1
+                for (int c = 0; c < D / 16; ++c) {
+                    uint32_t x[8], hi[4], lo[4];
+                    chunk(c, x);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        uint32_t h2[2], l2[2];
+#pragma unroll
+                        for (int y = 0; y < 2; ++y) {
+                            const float f0 = __uint_as_float(x[2 * i + y] << 16) * inv;
+                            const float f1 = __uint_as_float(x[2 * i + y] & 0xffff0000u) * inv;
+                            h2[y] = pack_e4m3(f0, f1);
+                            const float2 kept = float2_of(f16x2_of_e4m3x2(h2[y]));
+                            l2[y] = pack_e5m2(f0 - kept.x, f1 - kept.y);
+                        }
+                        hi[i] = h2[0] | h2[1] << 16;
+                        lo[i] = l2[0] | l2[1] << 16;
+                    }
+                    const int at = (D == 128 ? c ^ (tid & 7) : c ^ ((tid >> 1) & 3)) * 16;
+                    sts16(hi0 + at, make_uint4(hi[0], hi[1], hi[2], hi[3]));
+                    sts16(hi0 + C::TILE8 + at, make_uint4(lo[0], lo[1], lo[2], lo[3]));
+                }
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(q_full);
+            const int seen = visible(pc.cur.s, a.G, a.rows, pc.cur.rt, a.causal);
+            for (int k = pc.k0; k < pc.k1 && ok; ++k, ++j) {
+                q += RT;
+                if (!(ok = wwait(v_full + 8 * (j % VSTG), (uint32_t)(j / VSTG) & 1))) break;
+                if (!(ok = wwait(sc_full + 8 * (j % NSC), (uint32_t)(j / NSC) & 1))) break;
+                if (j >= 2 && !(ok = wwait(h_empty + 8 * (j & 1), (uint32_t)((j >> 1) - 1) & 1))) break;
+                const int left = seen - k * kTile;
+                const uint32_t src = sbase + C::V8_OFF + (j % VSTG) * C::TILE8, dst = sbase + C::V16_OFF + (j & 1) * C::TILE16;
+                constexpr int CH = D / 16;               // 16-code chunks of a row
+#pragma unroll 2
+                for (int i = 0; i < CH; ++i) {
+                    const int x = i * 128 + tid, r = x / CH, c = x % CH;
+                    uint4 v = lds16(src + x * 16);
+                    const bool live = r < left && sc_sh[(j % NSC) * 8 + (r >> 4)].w != 0.f;
+                    if (!live) v = make_uint4(0, 0, 0, 0);
+                    const uint4 lo = make_uint4(f16x2_of_e4m3x2(v.x), f16x2_of_e4m3x2_hi(v.x), f16x2_of_e4m3x2(v.y),
+                                                f16x2_of_e4m3x2_hi(v.y));
+                    const uint4 hi = make_uint4(f16x2_of_e4m3x2(v.z), f16x2_of_e4m3x2_hi(v.z), f16x2_of_e4m3x2(v.w),
+                                                f16x2_of_e4m3x2_hi(v.w));
+                    // atom c / 4 (64 channels), 16-byte chunks 2 (c % 4) and the next of its row;
+                    // odd atoms write theirs in the other order: no two lanes meet in a bank
+                    const uint32_t row = dst + (c >> 2) * (128 * 128) + r * 128;
+                    const uint32_t first = c >> 2 & 1, cc = 2 * (c & 3);
+                    sts16(row + (((cc + first) ^ (r & 7)) << 4), first ? hi : lo);
+                    sts16(row + (((cc + 1 - first) ^ (r & 7)) << 4), first ? lo : hi);
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(h_full + 8 * (j & 1));
+                    mbar_arrive(v_empty + 8 * (j % VSTG));
+                }
+            }
+        }
+    } else {
+        // ---------------- softmax ----------------
+        regs_inc<C::REG_SOFT>();
+        const int g = (warp - 8) >> 2, quad = warp & 3;
+        const int rig = quad * 32 + lane;                       // row of the group's 128 (TMEM lane)
+        const int row = RT == 2 ? g * 128 + rig : rig;
+        const uint32_t lane_off = (uint32_t)(quad * 32) << 16;
+        const uint32_t o_tmem = tmem + C::O_COL + g * D + lane_off;
+        int j = 0, units = 0;                                   // tiles so far; units of this group so far
+        uint32_t pieces = 0, soft_phase = 0;
+        bool ok = true;
+        auto soft_sync = [&]() -> bool {                        // all softmax warps
+            __syncwarp();
+            if (lane == 0) mbar_arrive(soft);
+            return wwait(soft, soft_phase++ & 1);
+        };
+        for (bool more = pc.begin(cur0); more && ok; more = pc.next(a)) {
+            if (!(ok = wwait(q_full, pieces & 1))) break;
+            ++pieces;
+            const float fac = factor[row];
+            __syncwarp();
+            if (lane == 0) mbar_arrive(q_read);
+            const RowPlace p = row_place(a, pc.cur.s, pc.cur.b, pc.cur.rt, pc.cur.h, row);
+            const int seen = visible(pc.cur.s, a.G, a.rows, pc.cur.rt, a.causal);
+            const int lim = p.valid ? p.limit : seen;
+            const int min_lim = imin(__reduce_min_sync(0xffffffffu, lim), seen);
+            float m = kNoMax, l = 0.f;
+            bool has = false;
+            for (int k = pc.k0; k < pc.k1; ++k, ++j) {
+                if (RT == 1 && (j & 1) != g) continue;
+                const int q = RT == 2 ? 2 * j + g : j, b = q % NB;
+                const uint32_t s_tmem = tmem + b * 128 + lane_off;
+                if (!(ok = wwait(sc_full + 8 * (j % NSC), (uint32_t)(j / NSC) & 1))) break;
+                if (!(ok = wwait(s_full + 8 * b, (uint32_t)(q / NB) & 1))) break;
+                tc_fence_after();
+                const float4 *const sc = sc_sh + (j % NSC) * 8;
+                const int n0 = k * kTile;
+                bool whole = n0 + kTile <= min_lim;
+                if (whole) whole = __all_sync(0xffffffffu, sc[lane & 7].w != 0.f);
+                uint32_t pw[64];
+                float sum, mx;
+                // weights of all 128 columns against reference m (packed into pw, their sum over
+                // 2^ev into `sum`), and the largest exponent
+                auto weights = [&](auto masked) {
+                    constexpr bool kMasked = decltype(masked)::value;
+                    sum = 0.f;
+                    mx = -INFINITY;
+                    uint32_t r[2][32];
+                    tmem_ld32(s_tmem, r[0]);
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        tmem_wait_ld();
+                        if (c < 3) tmem_ld32(s_tmem + 32 * (c + 1), r[(c + 1) & 1]);
+                        uint32_t(&x)[32] = r[c & 1];
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            const float4 f = sc[2 * c + h];
+                            const float kc = fac * f.x, add = f.y - m;
+                            const uint64_t kc2 = f2pack(kc, kc), add2_ = f2pack(add, add);
+                            uint64_t s2 = f2pack(0.f, 0.f);
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) {
+                                float u0, u1;
+                                f2unpack(fma2(f2pack(__uint_as_float(x[16 * h + 2 * i]), __uint_as_float(x[16 * h + 2 * i + 1])), kc2, add2_), u0, u1);
+                                if (kMasked) {
+                                    const int n = n0 + 32 * c + 16 * h + 2 * i;
+                                    if (n >= lim || f.w == 0.f) u0 = -INFINITY;
+                                    if (n + 1 >= lim || f.w == 0.f) u1 = -INFINITY;
+                                }
+                                mx = max3(mx, u0, u1);
+                                const float p0 = ex2(u0), p1 = ex2(u1);
+                                s2 = add2(s2, f2pack(p0, p1));
+                                pw[16 * c + 8 * h + i] = pack_f16(p0, p1);
+                            }
+                            float s0, s1;
+                            f2unpack(s2, s0, s1);
+                            sum = fmaf(s0 + s1, f.z, sum);
+                        }
+                    }
+                };
+                auto go = [&]() {
+                    if (whole) weights(std::false_type{});
+                    else weights(std::true_type{});
+                };
+                go();
+                if (__any_sync(0xffffffffu, mx > kHeadroom)) {
+                    // move the reference of the rows that need it: their largest exponent anew
+                    float best = -INFINITY;
+#pragma unroll 1
+                    for (int c = 0; c < 4; ++c) {
+                        uint32_t x[32];
+                        tmem_ld32(s_tmem + 32 * c, x);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) {
+                            const float4 f = sc[2 * c + (i >> 4)];
+                            const int n = n0 + 32 * c + i;
+                            if (n < lim && f.w != 0.f) best = fmaxf(best, fmaf(__uint_as_float(x[i]), fac * f.x, f.y));
+                        }
+                    }
+                    const float nm = best > m + kHeadroom ? best - kFresh : m;
+                    const float f = ex2(m - nm);
+                    if (has) {
+                        if (!(ok = wwait(o_done + 8 * g, (uint32_t)(units - 1) & 1))) break;
+                        tc_fence_after();
+#pragma unroll 1
+                        for (int c = 0; c < D / 16; ++c) {
+                            uint32_t o[16];
+                            tmem_ld16(o_tmem + c * 16, o);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+                            tmem_st16(o_tmem + c * 16, o);
+                        }
+                    }
+                    l *= f;
+                    m = nm;
+                    go();
+                }
+                l += sum;
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    uint32_t x[32];
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) x[i] = pw[32 * c + i];
+                    tmem_st32(s_tmem + 32 * c, x);
+                }
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(p_full + 8 * b);
+                has = true;
+                ++units;
+            }
+            if (!ok) break;
+            // ---- the item's rows (or this span's share of them) ----
+            if (has) {
+                if (!(ok = wwait(o_done + 8 * g, (uint32_t)(units - 1) & 1))) break;
+                tc_fence_after();
+            }
+            const bool final = pc.k0 == 0 && pc.k1 == pc.cur.nt;
+            const int64_t prow = ((int64_t)cta * 2 + (pc.k0 == 0 ? 1 : 0)) * a.rows + row;
+            float c0 = 1.f, c1 = 0.f, M = m, ls = l;
+            if (RT == 1) {
+                float2 *st = reinterpret_cast<float2 *>(smem + C::STAT_OFF);
+                st[g * 128 + rig] = make_float2(has ? m : kNoMax, has ? l : 0.f);
+                if (!(ok = soft_sync())) break;
+                tc_fence_after();
+                const float2 s0 = st[rig], s1 = st[128 + rig];
+                M = fmaxf(s0.x, s1.x);
+                c0 = s0.y == 0.f ? 0.f : ex2(s0.x - M);
+                c1 = s1.y == 0.f ? 0.f : ex2(s1.x - M);
+                ls = (c0 != 0.f ? c0 * s0.y : 0.f) + (c1 != 0.f ? c1 * s1.y : 0.f);
+            }
+            const float inv = !final ? 1.f : ls == 0.f ? 0.f : 1.f / ls;
+            c0 *= inv;
+            c1 *= inv;
+            // columns of this group: all of its own rows', or half of the shared rows'
+            constexpr int NCOL = RT == 2 ? D : D / 2;
+            const int col0 = RT == 2 ? 0 : g * (D / 2);
+#pragma unroll 1
+            for (int c = 0; c < NCOL / 16; ++c) {
+                const int col = col0 + 16 * c;
+                float v[16];
+                uint32_t r0[16], r1[16];
+                tmem_ld16((RT == 2 ? o_tmem : tmem + C::O_COL + lane_off) + col, r0);
+                if (RT == 1) tmem_ld16(tmem + C::O_COL + D + lane_off + col, r1);
+                tmem_wait_ld();
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const float x0 = c0 != 0.f ? c0 * __uint_as_float(r0[i]) : 0.f;      // an unused accumulator is not read
+                    const float x1 = RT == 1 && c1 != 0.f ? c1 * __uint_as_float(r1[i]) : 0.f;
+                    v[i] = x0 + x1;
+                }
+                if (p.valid) {
+                    if (!final) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            *reinterpret_cast<float4 *>(&a.part_O[prow * D + col + 4 * i]) =
+                                make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            store_o4(a, a.o_f32, p.o + col + 4 * i, make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]));
+                    }
+                }
+            }
+            if (p.valid && (RT == 2 || g == 0)) {
+                if (!final)
+                    a.part_ml[prow] = make_float2(M, ls);
+                else if (a.L)
+                    a.L[p.l] = ls == 0.f ? -INFINITY : (M + log2f(ls)) * kLn2;
+            }
+            tc_fence_before();
+            if (RT == 1 && !(ok = soft_sync())) break;          // both accumulators and the statistics are free
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 1) tmem_dealloc(tmem, 512);
+    pdl_launch_dependents();
+}
+
+// Codes as rows of D bytes; a box is a page's rows (128 at most).
+bool make_page_map(CUtensorMap *map, const void *base, const Pool &c, CUtensorMapSwizzle swizzle) {
+    auto fn = encode_fn();
+    if (!fn) return false;
+    const cuuint64_t dims[2] = {(cuuint64_t)c.D, (cuuint64_t)c.P * c.H * c.page};
+    const cuuint64_t strides[1] = {(cuuint64_t)c.D};
+    const cuuint32_t box[2] = {(cuuint32_t)c.D, (cuuint32_t)c.page};
+    const cuuint32_t estr[2] = {1, 1};
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(base), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D, int RT>
+cudaError_t launch_tc(const AttnArgs &a, cudaStream_t st) {
+    using C = TcCfg<D, RT>;
+    CUtensorMap mk, mv;
+    if (!make_page_map(&mk, a.c.k, a.c, D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B) ||
+        !make_page_map(&mv, a.c.v, a.c, CU_TENSOR_MAP_SWIZZLE_NONE))
+        return cudaErrorInvalidValue;
+    auto k = attn_tc_kernel<D, RT>;
+    cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::ALLOC);
+    if (e != cudaSuccess) return e;
+    // the warpgroups' register budgets (setmaxnreg) must add up to no more
+    // than the block's registers at launch, or an increase would wait forever
+    cudaFuncAttributes fa;
+    if ((e = cudaFuncGetAttributes(&fa, k)) != cudaSuccess) return e;
+    if ((uint32_t)fa.numRegs * 4 < C::REG_CTL + C::REG_CVT + 2 * C::REG_SOFT) return cudaErrorInvalidConfiguration;
+    k<<<a.grid, C::THREADS, C::ALLOC, st>>>(mk, mv, a);
+    note_launch();
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_attn_tc(const AttnArgs &a, cudaStream_t st) {
+    if (a.c.D == 128) return a.rows == 256 ? launch_tc<128, 2>(a, st) : launch_tc<128, 1>(a, st);
+    return a.rows == 256 ? launch_tc<64, 2>(a, st) : launch_tc<64, 1>(a, st);
+}
+
+}  // namespace cache
+}  // namespace flare

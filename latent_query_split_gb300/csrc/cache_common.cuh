@@ -70,6 +70,7 @@ AttnPlan attn_plan(const Pool &c, int G, bool bf16, int64_t T, int family, int s
 
 cudaError_t launch_attn(const AttnArgs &a, AttnKernel kernel, bool bf16, cudaStream_t st);
 cudaError_t launch_attn_mma(const AttnArgs &a, bool bf16, cudaStream_t st);
+cudaError_t launch_attn_tc(const AttnArgs &a, cudaStream_t st);
 cudaError_t launch_append(const AppendArgs &a, bool bf16, cudaStream_t st);
 
 }  // namespace cache
