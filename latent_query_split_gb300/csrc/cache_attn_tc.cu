@@ -68,8 +68,8 @@ struct TcCfg {
     static constexpr uint32_t BYTES = MISC_OFF + 16;
     static constexpr uint32_t ALLOC = BYTES + 1024;
     static_assert(ALLOC <= 232448, "shared memory budget of one CTA exceeded");
-    // registers per thread of each warpgroup: 128 at launch, 72 + 72 + 184 + 184 = 4 x 128
-    static constexpr uint32_t REG_CTL = 72, REG_CVT = 72, REG_SOFT = 184;
+    // registers per thread of each warpgroup: 128 at launch, 64 + 80 + 184 + 184 = 4 x 128
+    static constexpr uint32_t REG_CTL = 64, REG_CVT = 80, REG_SOFT = 184;
 };
 
 template <uint32_t R>
@@ -192,8 +192,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
         tmem_relinquish();
     }
     const Span sp = find_span<512>(a, cta, scan_sh, &cur_sh);
-    const Cursor cur0 = cur_sh;
-    if (threadIdx.x == 0) write_record(a, sp, cur0, cta);
+    if (threadIdx.x == 0) write_record(a, sp, cur_sh, cta);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -208,7 +207,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
             // read two batches ahead, scales one.
             int j = 0;
             bool ok = true;
-            for (bool more = pc.begin(cur0); more && ok; more = pc.next(a)) {
+            for (bool more = pc.begin(cur_sh); more && ok; more = pc.next(a)) {
                 const int seen = visible(pc.cur.s, a.G, a.rows, pc.cur.rt, a.causal);
                 const int32_t *const row_table = a.c.table + (int64_t)pc.cur.b * a.c.W;
                 const int nb = (pc.k1 - pc.k0 + 3) >> 2;
@@ -254,7 +253,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
                             const int ex = (int)((__float_as_uint(vs) >> 23) & 0xff);
                             *reinterpret_cast<float4 *>(smem + C::SC_OFF + (scl * 8 + grp) * 16) =
                                 page >= 0 ? make_float4(ks, (float)(ex - 127), __int_as_float((254 - ex) << 23), 1.f)
-                                          : make_float4(0.f, 0.f, 0.f, 0.f);
+                                          : make_float4(1.f, 0.f, 0.f, 0.f);
                         }
                         __syncwarp();
                         if (lane == 0) {
@@ -296,7 +295,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
             uint32_t pieces = 0;
             bool ok = true;
             auto desc = [&](uint32_t at) { return D == 128 ? desc_sw128(at, 16, 1024) : desc_sw64(at); };
-            for (bool more = pc.begin(cur0); more && ok; more = pc.next(a)) {
+            for (bool more = pc.begin(cur_sh); more && ok; more = pc.next(a)) {
                 if (!(ok = wwait(q_full, pieces++ & 1))) break;
                 for (int k = pc.k0; k < pc.k1 && ok; ++k, ++j) {
                     if (!(ok = wwait(k_full + 8 * (j % KSTG), (uint32_t)(j / KSTG) & 1))) break;
@@ -330,7 +329,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
             constexpr uint32_t idPV = idesc_f16(128, D, 0, 1);
             int j = 0, q = 0;
             bool ok = true;
-            for (bool more = pc.begin(cur0); more && ok; more = pc.next(a)) {
+            for (bool more = pc.begin(cur_sh); more && ok; more = pc.next(a)) {
                 bool fresh[2] = {true, true};
                 for (int k = pc.k0; k < pc.k1 && ok; ++k, ++j) {
                     const uint32_t vb = sbase + C::V16_OFF + (j & 1) * C::TILE16;
@@ -367,7 +366,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
         int j = 0, q = 0;
         uint32_t pieces = 0;
         bool ok = true;
-        for (bool more = pc.begin(cur0); more && ok; more = pc.next(a), ++pieces) {
+        for (bool more = pc.begin(cur_sh); more && ok; more = pc.next(a), ++pieces) {
             if (pieces > 0) {
                 // the last piece's factors have been read and its S products are done
                 if (!(ok = wwait(q_read, (pieces - 1) & 1))) break;
@@ -404,7 +403,8 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
                 }
                 const int e = imax((int)(top >> 23) - 127, -100);
                 const float inv = __int_as_float((7 - e + 127) << 23);
-                factor[g * 128 + tid] = top >= 0x7f800000u ? NAN : __int_as_float((e - 7 + 127) << 23) * a.sl2;
+                // (positive, so that -inf stays -inf; 1e-30 is as good as 0)
+                factor[g * 128 + tid] = top >= 0x7f800000u ? NAN : fmaxf(__int_as_float((e - 7 + 127) << 23) * a.sl2, 1e-30f);
                 const uint32_t hi0 = sbase + C::Q_OFF + g * 2 * C::TILE8 + tid * D;
 #pragma unroll 1
                 for (int c = 0; c < D / 16; ++c) {
@@ -441,22 +441,29 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
                 const int left = seen - k * kTile;
                 const uint32_t src = sbase + C::V8_OFF + (j % VSTG) * C::TILE8, dst = sbase + C::V16_OFF + (j & 1) * C::TILE16;
                 constexpr int CH = D / 16;               // 16-code chunks of a row
-#pragma unroll 2
-                for (int i = 0; i < CH; ++i) {
-                    const int x = i * 128 + tid, r = x / CH, c = x % CH;
-                    uint4 v = lds16(src + x * 16);
-                    const bool live = r < left && sc_sh[(j % NSC) * 8 + (r >> 4)].w != 0.f;
-                    if (!live) v = make_uint4(0, 0, 0, 0);
-                    const uint4 lo = make_uint4(f16x2_of_e4m3x2(v.x), f16x2_of_e4m3x2_hi(v.x), f16x2_of_e4m3x2(v.y),
-                                                f16x2_of_e4m3x2_hi(v.y));
-                    const uint4 hi = make_uint4(f16x2_of_e4m3x2(v.z), f16x2_of_e4m3x2_hi(v.z), f16x2_of_e4m3x2(v.w),
-                                                f16x2_of_e4m3x2_hi(v.w));
-                    // atom c / 4 (64 channels), 16-byte chunks 2 (c % 4) and the next of its row;
-                    // odd atoms write theirs in the other order: no two lanes meet in a bank
-                    const uint32_t row = dst + (c >> 2) * (128 * 128) + r * 128;
-                    const uint32_t first = c >> 2 & 1, cc = 2 * (c & 3);
-                    sts16(row + (((cc + first) ^ (r & 7)) << 4), first ? hi : lo);
-                    sts16(row + (((cc + 1 - first) ^ (r & 7)) << 4), first ? lo : hi);
+                const bool whole = __all_sync(0xffffffffu, left >= kTile && sc_sh[(j % NSC) * 8 + (lane & 7)].w != 0.f);
+                // thread tid's chunk i is number 128 i + tid of the tile: row r0 + i * 128 / CH,
+                // chunk c. It becomes two 16-byte chunks of atom c / 4 (64 channels); odd atoms
+                // write theirs in the other order, so that no two lanes meet in a bank.
+                const int r0 = tid / CH, c = tid % CH;
+                const uint32_t first = c >> 2 & 1, cc = 2 * (c & 3);
+#pragma unroll 1
+                for (int i0 = 0; i0 < CH; i0 += 4) {
+                    uint4 v[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) v[i] = lds16(src + ((i0 + i) * 128 + tid) * 16);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int r = r0 + (i0 + i) * (128 / CH);
+                        if (!whole && !(r < left && sc_sh[(j % NSC) * 8 + (r >> 4)].w != 0.f)) v[i] = make_uint4(0, 0, 0, 0);
+                        const uint4 lo = make_uint4(f16x2_of_e4m3x2(v[i].x), f16x2_of_e4m3x2_hi(v[i].x),
+                                                    f16x2_of_e4m3x2(v[i].y), f16x2_of_e4m3x2_hi(v[i].y));
+                        const uint4 hi = make_uint4(f16x2_of_e4m3x2(v[i].z), f16x2_of_e4m3x2_hi(v[i].z),
+                                                    f16x2_of_e4m3x2(v[i].w), f16x2_of_e4m3x2_hi(v[i].w));
+                        const uint32_t row = dst + (c >> 2) * (128 * 128) + r * 128;
+                        sts16(row + (((cc + first) ^ (r & 7)) << 4), first ? hi : lo);
+                        sts16(row + (((cc + 1 - first) ^ (r & 7)) << 4), first ? lo : hi);
+                    }
                 }
                 fence_proxy_async_smem();
                 __syncwarp();
@@ -482,7 +489,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
             if (lane == 0) mbar_arrive(soft);
             return wwait(soft, soft_phase++ & 1);
         };
-        for (bool more = pc.begin(cur0); more && ok; more = pc.next(a)) {
+        for (bool more = pc.begin(cur_sh); more && ok; more = pc.next(a)) {
             if (!(ok = wwait(q_full, pieces & 1))) break;
             ++pieces;
             const float fac = factor[row];
@@ -503,95 +510,81 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
                 tc_fence_after();
                 const float4 *const sc = sc_sh + (j % NSC) * 8;
                 const int n0 = k * kTile;
-                bool whole = n0 + kTile <= min_lim;
-                if (whole) whole = __all_sync(0xffffffffu, sc[lane & 7].w != 0.f);
-                uint32_t pw[64];
-                float sum, mx;
-                // weights of all 128 columns against reference m (packed into pw, their sum over
-                // 2^ev into `sum`), and the largest exponent
-                auto weights = [&](auto masked) {
-                    constexpr bool kMasked = decltype(masked)::value;
-                    sum = 0.f;
-                    mx = -INFINITY;
-                    uint32_t r[2][32];
-                    tmem_ld32(s_tmem, r[0]);
+                const bool whole = __all_sync(0xffffffffu, n0 + kTile <= min_lim && sc[lane & 7].w != 0.f);
+                // the row's 128 products; hidden ones become -inf
+                uint32_t x[4][32];
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        tmem_wait_ld();
-                        if (c < 3) tmem_ld32(s_tmem + 32 * (c + 1), r[(c + 1) & 1]);
-                        uint32_t(&x)[32] = r[c & 1];
+                for (int c = 0; c < 4; ++c) tmem_ld32(s_tmem + 32 * c, x[c]);
+                tmem_wait_ld();
+                if (!whole) {
 #pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            const float4 f = sc[2 * c + h];
-                            const float kc = fac * f.x, add = f.y - m;
-                            const uint64_t kc2 = f2pack(kc, kc), add2_ = f2pack(add, add);
-                            uint64_t s2 = f2pack(0.f, 0.f);
+                    for (int c = 0; c < 4; ++c)
 #pragma unroll
-                            for (int i = 0; i < 8; ++i) {
-                                float u0, u1;
-                                f2unpack(fma2(f2pack(__uint_as_float(x[16 * h + 2 * i]), __uint_as_float(x[16 * h + 2 * i + 1])), kc2, add2_), u0, u1);
-                                if (kMasked) {
-                                    const int n = n0 + 32 * c + 16 * h + 2 * i;
-                                    if (n >= lim || f.w == 0.f) u0 = -INFINITY;
-                                    if (n + 1 >= lim || f.w == 0.f) u1 = -INFINITY;
-                                }
-                                mx = max3(mx, u0, u1);
-                                const float p0 = ex2(u0), p1 = ex2(u1);
-                                s2 = add2(s2, f2pack(p0, p1));
-                                pw[16 * c + 8 * h + i] = pack_f16(p0, p1);
-                            }
-                            float s0, s1;
-                            f2unpack(s2, s0, s1);
-                            sum = fmaf(s0 + s1, f.z, sum);
-                        }
+                        for (int i = 0; i < 32; ++i)
+                            if (n0 + 32 * c + i >= lim || sc[2 * c + (i >> 4)].w == 0.f) x[c][i] = 0xff800000u;
+                }
+                // the largest exponent: a maximum of products in each page group, scaled once
+                // (the factors are positive)
+                float best = -INFINITY;
+#pragma unroll
+                for (int h = 0; h < 8; ++h) {
+                    const uint32_t *const y = &x[h >> 1][16 * (h & 1)];
+                    const float4 f = sc[h];
+                    float a0 = __uint_as_float(y[0]), a1 = __uint_as_float(y[1]);
+#pragma unroll
+                    for (int i = 2; i < 16; i += 4) {
+                        a0 = max3(a0, __uint_as_float(y[i]), __uint_as_float(y[i + 1]));
+                        if (i + 2 < 16) a1 = max3(a1, __uint_as_float(y[i + 2]), __uint_as_float(y[i + 3]));
                     }
-                };
-                auto go = [&]() {
-                    if (whole) weights(std::false_type{});
-                    else weights(std::true_type{});
-                };
-                go();
-                if (__any_sync(0xffffffffu, mx > kHeadroom)) {
-                    // move the reference of the rows that need it: their largest exponent anew
-                    float best = -INFINITY;
-#pragma unroll 1
-                    for (int c = 0; c < 4; ++c) {
-                        uint32_t x[32];
-                        tmem_ld32(s_tmem + 32 * c, x);
-                        tmem_wait_ld();
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) {
-                            const float4 f = sc[2 * c + (i >> 4)];
-                            const int n = n0 + 32 * c + i;
-                            if (n < lim && f.w != 0.f) best = fmaxf(best, fmaf(__uint_as_float(x[i]), fac * f.x, f.y));
-                        }
-                    }
+                    best = fmaxf(best, fmaf(fmaxf(a0, a1), fac * f.x, f.y));
+                }
+                if (__any_sync(0xffffffffu, best > m + kHeadroom)) {
+                    // move the reference of the rows that need it
                     const float nm = best > m + kHeadroom ? best - kFresh : m;
                     const float f = ex2(m - nm);
                     if (has) {
                         if (!(ok = wwait(o_done + 8 * g, (uint32_t)(units - 1) & 1))) break;
                         tc_fence_after();
 #pragma unroll 1
-                        for (int c = 0; c < D / 16; ++c) {
-                            uint32_t o[16];
-                            tmem_ld16(o_tmem + c * 16, o);
+                        for (int c = 0; c < D / 32; ++c) {
+                            uint32_t o0[16], o1[16];
+                            tmem_ld16(o_tmem + c * 32, o0);
+                            tmem_ld16(o_tmem + c * 32 + 16, o1);
                             tmem_wait_ld();
 #pragma unroll
-                            for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-                            tmem_st16(o_tmem + c * 16, o);
+                            for (int i = 0; i < 16; ++i) {
+                                o0[i] = __float_as_uint(__uint_as_float(o0[i]) * f);
+                                o1[i] = __float_as_uint(__uint_as_float(o1[i]) * f);
+                            }
+                            tmem_st16(o_tmem + c * 32, o0);
+                            tmem_st16(o_tmem + c * 32 + 16, o1);
                         }
                     }
                     l *= f;
                     m = nm;
-                    go();
                 }
-                l += sum;
 #pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    uint32_t x[32];
+                for (int c = 0; c < 4; ++c) {
+                    uint32_t pw[16];
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) x[i] = pw[32 * c + i];
-                    tmem_st32(s_tmem + 32 * c, x);
+                    for (int h = 0; h < 2; ++h) {
+                        const float4 f = sc[2 * c + h];
+                        const float kc = fac * f.x, add = f.y - m;
+                        const uint64_t kc2 = f2pack(kc, kc), ad2 = f2pack(add, add);
+                        uint64_t s2 = f2pack(0.f, 0.f);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            float u0, u1;
+                            f2unpack(fma2(f2pack(__uint_as_float(x[c][16 * h + 2 * i]), __uint_as_float(x[c][16 * h + 2 * i + 1])), kc2, ad2), u0, u1);
+                            const float p0 = ex2(u0), p1 = ex2(u1);
+                            s2 = add2(s2, f2pack(p0, p1));
+                            pw[8 * h + i] = pack_f16(p0, p1);
+                        }
+                        float s0, s1;
+                        f2unpack(s2, s0, s1);
+                        l = fmaf(s0 + s1, f.z, l);
+                    }
+                    tmem_st16(s_tmem + 16 * c, pw);
                 }
                 tmem_wait_st();
                 tc_fence_before();
