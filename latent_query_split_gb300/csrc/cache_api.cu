@@ -63,6 +63,9 @@ flare_status_t check_rows(const flare_cache_dims_t *d, int64_t T, const int32_t 
     if (T < 0 || T > (1ll << 31) - 1) return fail(FLARE_ERR_INVALID_ARG, "T=%lld outside [0, 2^31)", (long long)T);
     if (!lens || !aligned(lens, 4) || !aligned(cu, 4))
         return fail(FLARE_ERR_INVALID_ARG, "seq_lens is required, and int32 tensors must be 4-byte aligned");
+    if (d->Hq > 0 && T * (d->Hq / d->H) > (1ll << 31) - 512)
+        return fail(FLARE_ERR_UNSUPPORTED, "T=%lld rows of %d query heads a head: 2^31 - 512 at most together", (long long)T,
+                    d->Hq / d->H);
     if (!cu && d->B > 0 && T % d->B)
         return fail(FLARE_ERR_INVALID_ARG, "T=%lld rows are not B=%d equal sequences (no cu_seqlens)", (long long)T, d->B);
     return FLARE_OK;

@@ -20,13 +20,17 @@
 //               slots may hold NaN codes, and 0 * NaN is not 0.
 //   l += 2^-ev sum w.
 //
-// Roles (16 warps): 0 fetches pages and scales, 1 issues O += w V, 2 issues S,
-// 3 is idle, 4-7 stage Q and convert V, 8-11 and 12-15 are two softmax groups.
-// RT = 2: group g has rows 128 g ..; RT = 1: the groups take tiles in turn, each
-// with an accumulator of its own, joined at the end of the item. Unit q = (tile,
-// group) in order; its S lies in TMEM buffer q % NB, of which 512 columns hold
-// two beside two 128-channel accumulators and three beside 64-channel ones. So
-// one group's products run under the other's exponentials.
+// Roles (16 warps): 0 fetches pages and scales, 1 issues O += w V, 2 issues S
+// (two issuers: the waits of one run under the other's products), 3 is idle, 4-7
+// stage Q and convert V, 8-11 and 12-15 are two softmax groups. RT = 2: group g
+// has rows 128 g ..; RT = 1: the groups take tiles in turn, each with an
+// accumulator of its own, joined at the end of the item. Unit q = (tile, group),
+// in order, belongs to group q % 2, which has one 128-column buffer for its
+// scores; one group's products run under the other's exponentials.
+//   D = 128: the two buffers and the two accumulators fill the 512 columns; w
+//   takes the scores' place, and S of unit q + 2 waits for O += w V of unit q.
+//   D = 64: w has columns of its own, so S of unit q + 2 is issued as soon as
+//   the group holds the weights of unit q in registers.
 #include "cache_device.cuh"
 #include "tc_host.cuh"
 
@@ -37,22 +41,24 @@ namespace {
 using namespace tc;
 
 constexpr float kNoMax = -3.0e38f;
-constexpr float kHeadroom = 15.f;        // w <= 2^15: fp16 holds 65504
-constexpr float kFresh = 7.f;            // a new largest score starts at w = 2^7
+constexpr float kMaxSum = 60000.f;       // of 16 weights: fp16 holds 65504
+constexpr float kOver = 11.5f;           // the largest exponent of such a sum is over this
+constexpr int kTries = 1 << 23;          // of a wait: a second at least
+constexpr float kFresh = 8.f;            // a new largest weight is 2^8 at most
 
 template <int D_, int RT_>
 struct TcCfg {
     static constexpr int D = D_, RT = RT_;
     static constexpr int ROWS = 128 * RT;
     static constexpr int THREADS = 512;
-    static constexpr int NB = D == 128 ? 2 : 3;                        // S buffers
+    static constexpr bool SEP = D == 64;                               // w in columns of its own
     static constexpr int KSTG = D == 128 ? (RT == 2 ? 3 : 4) : 6;      // key stages
     static constexpr int VSTG = D == 128 ? (RT == 2 ? 2 : 3) : 6;      // value stages (codes)
-    // a tile's scales outlive its stages by the units between S and O
+    // a tile's scales outlive its key stage by the two units between S and w
     static constexpr int NSC = 16;
-    static_assert(NSC >= KSTG + NB + 1, "scale ring too short");
-    static constexpr uint32_t O_COL = NB * 128;
-    static_assert(O_COL + 2 * D <= 512, "tensor-memory columns exceeded");
+    static_assert(NSC >= KSTG + 3, "scale ring too short");
+    static constexpr uint32_t O_COL = 256, P_COL = O_COL + 2 * D;      // group g: scores at 128 g
+    static_assert(P_COL + (SEP ? 128 : 0) <= 512, "tensor-memory columns exceeded");
     static constexpr uint32_t TILE8 = 128 * D;                         // a tile of codes
     static constexpr uint32_t TILE16 = 2 * TILE8;
     static constexpr uint32_t Q_OFF = 0;                               // per row tile: e4m3 part, e5m2 part
@@ -63,23 +69,12 @@ struct TcCfg {
     static constexpr uint32_t FAC_OFF = SC_OFF + NSC * 8 * 16;         // [ROWS] row factors
     static constexpr uint32_t STAT_OFF = FAC_OFF + ROWS * 4;           // RT = 1: [2][128] (m, l)
     static constexpr uint32_t BAR_OFF = STAT_OFF + (RT == 1 ? 2048 : 0);
-    static constexpr int NBAR = 2 * KSTG + 2 * VSTG + NSC + 4 + 2 + 3 * NB + 2 + 3;
+    static constexpr int NBAR = 2 * KSTG + 2 * VSTG + NSC + 4 + 2 + 6 + 2 + 3;
     static constexpr uint32_t MISC_OFF = BAR_OFF + NBAR * 8;
     static constexpr uint32_t BYTES = MISC_OFF + 16;
     static constexpr uint32_t ALLOC = BYTES + 1024;
     static_assert(ALLOC <= 232448, "shared memory budget of one CTA exceeded");
-    // registers per thread of each warpgroup: 128 at launch, 64 + 80 + 184 + 184 = 4 x 128
-    static constexpr uint32_t REG_CTL = 64, REG_CVT = 80, REG_SOFT = 184;
 };
-
-template <uint32_t R>
-__device__ __forceinline__ void regs_inc() {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R));
-}
-template <uint32_t R>
-__device__ __forceinline__ void regs_dec() {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R));
-}
 
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
     uint32_t r;
@@ -103,6 +98,19 @@ __device__ __forceinline__ uint4 lds16(uint32_t a) {
 }
 __device__ __forceinline__ void sts16(uint32_t a, uint4 v) {
     asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+
+// The rest of a wait that was not over at once. Every try may suspend the warp for a
+// while; counting tries instead of reading a clock keeps the loop short, as other warps
+// want the issue slots.
+static __device__ __noinline__ bool wait_on(uint32_t bar, uint32_t par, volatile int *abort_flag, unsigned *status) {
+    for (int i = 0; i < kTries; ++i) {
+        if (__all_sync(0xffffffffu, mbar_try_wait(bar, par))) return true;
+        if (*abort_flag) return false;
+    }
+    *abort_flag = 1;
+    atomicCAS(status, 0u, 1u);
+    return false;
 }
 
 // The pieces of a CTA's span, in order: what every role walks.
@@ -131,7 +139,8 @@ template <int D, int RT>
 __global__ void __launch_bounds__(512, 1)
 attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const AttnArgs a) {
     using C = TcCfg<D, RT>;
-    constexpr int NB = C::NB, KSTG = C::KSTG, VSTG = C::VSTG, NSC = C::NSC;
+    constexpr int KSTG = C::KSTG, VSTG = C::VSTG, NSC = C::NSC;
+    constexpr bool SEP = C::SEP;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     __shared__ int64_t scan_sh[16];
@@ -145,16 +154,18 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
         return b;
     };
     const uint32_t k_full = bars(KSTG), k_empty = bars(KSTG), v_full = bars(VSTG), v_empty = bars(VSTG), sc_full = bars(NSC),
-                   h_full = bars(2), h_empty = bars(2), q_full = bars(1), q_read = bars(1), s_full = bars(NB),
-                   p_full = bars(NB), buf_free = bars(NB), o_done = bars(2), soft = bars(1), drain = bars(2);
+                   h_full = bars(2), h_empty = bars(2), q_full = bars(1), q_read = bars(1), s_full = bars(2),
+                   s_free = bars(2), p_full = bars(2), o_done = bars(2), soft = bars(1), drain = bars(2);
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::MISC_OFF);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + C::MISC_OFF + 4);
     const float4 *const sc_sh = reinterpret_cast<const float4 *>(smem + C::SC_OFF);
     float *const factor = reinterpret_cast<float *>(smem + C::FAC_OFF);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, cta = blockIdx.x;
-    Waiter wt{abort_flag, a.status};
-    auto wwait = [&](uint32_t bar, uint32_t par) -> bool { return __all_sync(0xffffffffu, wt.wait_inline(bar, par)); };
+    // A bounded wait of a whole warp.
+    auto wwait = [&](uint32_t bar, uint32_t par) -> bool {
+        return __all_sync(0xffffffffu, mbar_try_wait(bar, par)) || wait_on(bar, par, abort_flag, a.status);
+    };
 
     if (threadIdx.x == 0) {
         *abort_flag = 0;
@@ -170,16 +181,15 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
         for (int s = 0; s < 2; ++s) {
             mbar_init(h_full + 8 * s, 4);
             mbar_init(h_empty + 8 * s, 1);
+            mbar_init(s_full + 8 * s, 1);
+            mbar_init(s_free + 8 * s, SEP ? 4 : 1);  // the group's warps, or a commit
+            mbar_init(p_full + 8 * s, 4);
             mbar_init(o_done + 8 * s, 1);
-            mbar_init(drain + 8 * s, 1);
         }
+        mbar_init(drain, 1);
+        mbar_init(drain + 8, 1);
         mbar_init(q_full, 4);
         mbar_init(q_read, 8);                        // the softmax warps
-        for (int b = 0; b < NB; ++b) {
-            mbar_init(s_full + 8 * b, 1);
-            mbar_init(p_full + 8 * b, 4);            // the owning group's warps
-            mbar_init(buf_free + 8 * b, 1);
-        }
         mbar_init(soft, 8);
         fence_mbar_init();
     }
@@ -200,13 +210,13 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
     Piece pc;
 
     if (warp < 4) {
-        regs_dec<C::REG_CTL>();
         if (warp == 0) {
             // ---------------- pages and scales ----------------
             // Lane i holds group i (16 tokens) of four tiles at a time; page numbers are
             // read two batches ahead, scales one.
             int j = 0;
             bool ok = true;
+#pragma unroll 1
             for (bool more = pc.begin(cur_sh); more && ok; more = pc.next(a)) {
                 const int seen = visible(pc.cur.s, a.G, a.rows, pc.cur.rt, a.causal);
                 const int32_t *const row_table = a.c.table + (int64_t)pc.cur.b * a.c.W;
@@ -233,11 +243,13 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
                     }
                 };
                 scales(page, ks, vs);
+#pragma unroll 1
                 for (int batch = 0; batch < nb && ok; ++batch) {
                     const int npage = checked(page1);
                     float nks, nvs;
                     scales(npage, nks, nvs);
                     page1 = page_of_batch(batch + 2);
+#pragma unroll 1
                     for (int sub = 0; sub < 4 && ok; ++sub) {
                         const int k = pc.k0 + 4 * batch + sub;
                         if (k >= pc.k1) break;
@@ -278,7 +290,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
                     vs = nvs;
                 }
             }
-            if (wt.aborted() && lane == 0) {
+            if (*abort_flag && lane == 0) {
                 // every issued copy lands before the CTA goes
                 const uint64_t t0 = globaltimer();
                 for (int x = j > KSTG ? j - KSTG : 0; x < j; ++x)
@@ -291,33 +303,35 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
         } else if (warp == 2) {
             // ---------------- S = Q K^T ----------------
             constexpr uint32_t idHi = idesc_f8(128, 128, 0), idLo = idesc_f8(128, 128, 1);
+            auto desc = [&](uint32_t at) { return D == 128 ? desc_sw128(at, 16, 1024) : desc_sw64(at); };
             int j = 0, q = 0;
             uint32_t pieces = 0;
             bool ok = true;
-            auto desc = [&](uint32_t at) { return D == 128 ? desc_sw128(at, 16, 1024) : desc_sw64(at); };
+#pragma unroll 1
             for (bool more = pc.begin(cur_sh); more && ok; more = pc.next(a)) {
                 if (!(ok = wwait(q_full, pieces++ & 1))) break;
+#pragma unroll 1
                 for (int k = pc.k0; k < pc.k1 && ok; ++k, ++j) {
                     if (!(ok = wwait(k_full + 8 * (j % KSTG), (uint32_t)(j / KSTG) & 1))) break;
                     const uint64_t dK = desc(sbase + C::K_OFF + (j % KSTG) * C::TILE8);
-#pragma unroll
-                    for (int g = 0; g < RT; ++g, ++q) {
-                        const int b = q % NB;
-                        if (q >= NB && !(ok = wwait(buf_free + 8 * b, (uint32_t)(q / NB - 1) & 1))) break;
+#pragma unroll 1
+                    for (int u = 0; u < RT; ++u, ++q) {
+                        const int g = q & 1;
+                        // the buffer's scores have been read (its weights, where they take that place)
+                        if (q >= 2 && !(ok = wwait(s_free + 8 * g, (uint32_t)((q >> 1) - 1) & 1))) break;
                         tc_fence_after();
-                        const uint64_t dHi = desc(sbase + C::Q_OFF + g * 2 * C::TILE8);
-                        const uint64_t dLo = desc(sbase + C::Q_OFF + (g * 2 + 1) * C::TILE8);
+                        const uint64_t dHi = desc(sbase + C::Q_OFF + u * 2 * C::TILE8), dLo = desc(sbase + C::Q_OFF + (u * 2 + 1) * C::TILE8);
 #pragma unroll
                         for (int kb = 0; kb < D / 32; ++kb) {
-                            umma_f8_ss_elect(tmem + b * 128, dHi + 2 * kb, dK + 2 * kb, idHi, kb > 0);
-                            umma_f8_ss_elect(tmem + b * 128, dLo + 2 * kb, dK + 2 * kb, idLo, 1u);
+                            umma_f8_ss_elect(tmem + g * 128, dHi + 2 * kb, dK + 2 * kb, idHi, kb > 0);
+                            umma_f8_ss_elect(tmem + g * 128, dLo + 2 * kb, dK + 2 * kb, idLo, 1u);
                         }
-                        umma_commit_elect(s_full + 8 * b);
+                        umma_commit_elect(s_full + 8 * g);
                     }
                     if (ok) umma_commit_elect(k_empty + 8 * (j % KSTG));
                 }
             }
-            if (wt.aborted()) {
+            if (*abort_flag) {
                 umma_commit_elect(drain);
                 const uint64_t t0 = globaltimer();
                 while (!mbar_try_wait(drain, 0) && globaltimer() - t0 < 500000000ull) {
@@ -329,29 +343,31 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
             constexpr uint32_t idPV = idesc_f16(128, D, 0, 1);
             int j = 0, q = 0;
             bool ok = true;
+#pragma unroll 1
             for (bool more = pc.begin(cur_sh); more && ok; more = pc.next(a)) {
                 bool fresh[2] = {true, true};
+#pragma unroll 1
                 for (int k = pc.k0; k < pc.k1 && ok; ++k, ++j) {
-                    const uint32_t vb = sbase + C::V16_OFF + (j & 1) * C::TILE16;
-                    const uint64_t dV = desc_sw128(vb, 128 * 128, 1024);
-#pragma unroll
+                    const uint64_t dV = desc_sw128(sbase + C::V16_OFF + (j & 1) * C::TILE16, 128 * 128, 1024);
+#pragma unroll 1
                     for (int u = 0; u < RT; ++u, ++q) {
-                        const int g = q & 1, b = q % NB;
-                        if (!(ok = wwait(p_full + 8 * b, (uint32_t)(q / NB) & 1))) break;
+                        const int g = q & 1;
                         if (u == 0 && !(ok = wwait(h_full + 8 * (j & 1), (uint32_t)(j >> 1) & 1))) break;
+                        if (!(ok = wwait(p_full + 8 * g, (uint32_t)(q >> 1) & 1))) break;
                         tc_fence_after();
+                        const uint32_t tP = tmem + (SEP ? C::P_COL + g * 64 : g * 128);
 #pragma unroll
                         for (int kb = 0; kb < 8; ++kb)
-                            umma_ts_elect(tmem + C::O_COL + g * D, tmem + b * 128 + kb * 8, dV + (uint64_t)(kb * 16 * 128 >> 4),
-                                          idPV, kb > 0 || !fresh[g]);
+                            umma_ts_elect(tmem + C::O_COL + g * D, tP + kb * 8, dV + (uint64_t)(kb * 16 * 128 >> 4), idPV,
+                                          kb > 0 || !fresh[g]);
                         fresh[g] = false;
+                        if (!SEP) umma_commit_elect(s_free + 8 * g);
                         umma_commit_elect(o_done + 8 * g);
-                        umma_commit_elect(buf_free + 8 * b);
                     }
                     if (ok) umma_commit_elect(h_empty + 8 * (j & 1));
                 }
             }
-            if (wt.aborted()) {
+            if (*abort_flag) {
                 umma_commit_elect(drain + 8);
                 const uint64_t t0 = globaltimer();
                 while (!mbar_try_wait(drain + 8, 0) && globaltimer() - t0 < 500000000ull) {
@@ -361,78 +377,72 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
         }
     } else if (warp < 8) {
         // ---------------- Q into two 8-bit parts; V into fp16 ----------------
-        regs_dec<C::REG_CVT>();
         const int tid = threadIdx.x - 128;           // 0 .. 127
         int j = 0, q = 0;
         uint32_t pieces = 0;
         bool ok = true;
+#pragma unroll 1
         for (bool more = pc.begin(cur_sh); more && ok; more = pc.next(a), ++pieces) {
             if (pieces > 0) {
                 // the last piece's factors have been read and its S products are done
                 if (!(ok = wwait(q_read, (pieces - 1) & 1))) break;
-                if (!(ok = wwait(s_full + 8 * ((q - 1) % NB), (uint32_t)((q - 1) / NB) & 1))) break;
+                if (!(ok = wwait(s_full + 8 * ((q - 1) & 1), (uint32_t)((q - 1) >> 1) & 1))) break;
             }
+            // D / 8 lanes take a row, 8 channels each; eight rows of a lane are loaded at once
+            constexpr int LR = D / 8, RW = 32 / LR;              // lanes a row, rows a warp and load
+            const int rl = lane / LR, c = lane % LR;
 #pragma unroll 1
-            for (int g = 0; g < RT; ++g) {
-                const RowPlace p = row_place(a, pc.cur.s, pc.cur.b, pc.cur.rt, pc.cur.h, g * 128 + tid);
-                const __nv_bfloat16 *src = reinterpret_cast<const __nv_bfloat16 *>(a.Q) + p.q;
-                const bool vec = (reinterpret_cast<uintptr_t>(src) & 15) == 0;
-                auto chunk = [&](int c, uint32_t (&x)[8]) {          // 16 channels, bf16 pairs
-                    if (!p.valid) {
+            for (int r0 = (warp - 4) * (C::ROWS / 4); r0 < (warp - 3) * (C::ROWS / 4); r0 += 8 * RW) {
+                uint4 v[8];
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) x[i] = 0u;
-                    } else if (vec) {
-                        const uint4 u = reinterpret_cast<const uint4 *>(src)[2 * c], v = reinterpret_cast<const uint4 *>(src)[2 * c + 1];
-                        x[0] = u.x; x[1] = u.y; x[2] = u.z; x[3] = u.w;
-                        x[4] = v.x; x[5] = v.y; x[6] = v.z; x[7] = v.w;
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            const __nv_bfloat162 y = __halves2bfloat162(src[16 * c + 2 * i], src[16 * c + 2 * i + 1]);
-                            x[i] = *reinterpret_cast<const uint32_t *>(&y);
+                for (int i = 0; i < 8; ++i) {
+                    const RowPlace p = row_place(a, pc.cur.s, pc.cur.b, pc.cur.rt, pc.cur.h, r0 + i * RW + rl);
+                    const __nv_bfloat16 *src = reinterpret_cast<const __nv_bfloat16 *>(a.Q) + p.q + 8 * c;
+                    v[i] = make_uint4(0, 0, 0, 0);
+                    if (p.valid) {
+                        if ((reinterpret_cast<uintptr_t>(src) & 15) == 0) {
+                            v[i] = *reinterpret_cast<const uint4 *>(src);
+                        } else {
+                            const uint16_t *s = reinterpret_cast<const uint16_t *>(src);
+                            v[i] = make_uint4(s[0] | (uint32_t)s[1] << 16, s[2] | (uint32_t)s[3] << 16,
+                                              s[4] | (uint32_t)s[5] << 16, s[6] | (uint32_t)s[7] << 16);
                         }
                     }
-                };
-                uint32_t top = 0;
-#pragma unroll 1
-                for (int c = 0; c < D / 16; ++c) {
-                    uint32_t x[8];
-                    chunk(c, x);
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) top = max(top, max(x[i] & 0x7fff0000u, (x[i] & 0x7fffu) << 16));
                 }
-                const int e = imax((int)(top >> 23) - 127, -100);
-                const float inv = __int_as_float((7 - e + 127) << 23);
-                // (positive, so that -inf stays -inf; 1e-30 is as good as 0)
-                factor[g * 128 + tid] = top >= 0x7f800000u ? NAN : fmaxf(__int_as_float((e - 7 + 127) << 23) * a.sl2, 1e-30f);
-                const uint32_t hi0 = sbase + C::Q_OFF + g * 2 * C::TILE8 + tid * D;
-#pragma unroll 1
-                for (int c = 0; c < D / 16; ++c) {
-                    uint32_t x[8], hi[4], lo[4];
-                    chunk(c, x);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        uint32_t h2[2], l2[2];
+                for (int i = 0; i < 8; ++i) {
+                    const int r = r0 + i * RW + rl, g = r >> 7, rg = r & 127;
+                    const uint32_t x[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+                    uint32_t top = 0;
 #pragma unroll
-                        for (int y = 0; y < 2; ++y) {
-                            const float f0 = __uint_as_float(x[2 * i + y] << 16) * inv;
-                            const float f1 = __uint_as_float(x[2 * i + y] & 0xffff0000u) * inv;
-                            h2[y] = pack_e4m3(f0, f1);
-                            const float2 kept = float2_of(f16x2_of_e4m3x2(h2[y]));
-                            l2[y] = pack_e5m2(f0 - kept.x, f1 - kept.y);
-                        }
-                        hi[i] = h2[0] | h2[1] << 16;
-                        lo[i] = l2[0] | l2[1] << 16;
+                    for (int y = 0; y < 4; ++y) top = max(top, max(x[y] & 0x7fff0000u, (x[y] & 0x7fffu) << 16));
+#pragma unroll
+                    for (int y = LR / 2; y; y >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, y));
+                    const int e = imax((int)(top >> 23) - 127, -100);
+                    const float inv = __int_as_float((7 - e + 127) << 23);
+                    // (positive, so that -inf stays -inf; 1e-30 is as good as 0)
+                    if (c == 0)
+                        factor[r] = top >= 0x7f800000u ? NAN : fmaxf(__int_as_float((e - 7 + 127) << 23) * a.sl2, 1e-30f);
+                    uint32_t hi[4], lo[4];
+#pragma unroll
+                    for (int y = 0; y < 4; ++y) {
+                        const float f0 = __uint_as_float(x[y] << 16) * inv, f1 = __uint_as_float(x[y] & 0xffff0000u) * inv;
+                        hi[y] = pack_e4m3(f0, f1);
+                        const float2 kept = float2_of(f16x2_of_e4m3x2(hi[y]));
+                        lo[y] = pack_e5m2(f0 - kept.x, f1 - kept.y);
                     }
-                    const int at = (D == 128 ? c ^ (tid & 7) : c ^ ((tid >> 1) & 3)) * 16;
-                    sts16(hi0 + at, make_uint4(hi[0], hi[1], hi[2], hi[3]));
-                    sts16(hi0 + C::TILE8 + at, make_uint4(lo[0], lo[1], lo[2], lo[3]));
+                    const int ch = c >> 1;                        // 16-byte chunk of the row of codes
+                    const uint32_t at = sbase + C::Q_OFF + g * 2 * C::TILE8 + rg * D +
+                                        (D == 128 ? ch ^ (rg & 7) : ch ^ ((rg >> 1) & 3)) * 16 + 8 * (c & 1);
+                    asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(at), "r"(hi[0] | hi[1] << 16), "r"(hi[2] | hi[3] << 16) : "memory");
+                    asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(at + C::TILE8), "r"(lo[0] | lo[1] << 16), "r"(lo[2] | lo[3] << 16) : "memory");
                 }
             }
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(q_full);
             const int seen = visible(pc.cur.s, a.G, a.rows, pc.cur.rt, a.causal);
+#pragma unroll 1
             for (int k = pc.k0; k < pc.k1 && ok; ++k, ++j) {
                 q += RT;
                 if (!(ok = wwait(v_full + 8 * (j % VSTG), (uint32_t)(j / VSTG) & 1))) break;
@@ -475,7 +485,6 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
         }
     } else {
         // ---------------- softmax ----------------
-        regs_inc<C::REG_SOFT>();
         const int g = (warp - 8) >> 2, quad = warp & 3;
         const int rig = quad * 32 + lane;                       // row of the group's 128 (TMEM lane)
         const int row = RT == 2 ? g * 128 + rig : rig;
@@ -489,6 +498,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
             if (lane == 0) mbar_arrive(soft);
             return wwait(soft, soft_phase++ & 1);
         };
+#pragma unroll 1
         for (bool more = pc.begin(cur_sh); more && ok; more = pc.next(a)) {
             if (!(ok = wwait(q_full, pieces & 1))) break;
             ++pieces;
@@ -499,97 +509,172 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
             const int seen = visible(pc.cur.s, a.G, a.rows, pc.cur.rt, a.causal);
             const int lim = p.valid ? p.limit : seen;
             const int min_lim = imin(__reduce_min_sync(0xffffffffu, lim), seen);
+            const bool idle = !__any_sync(0xffffffffu, p.valid);
+            // where a new largest weight starts: the fp16 weights that round to zero, under
+            // 2^-25, stay 2^-10 of the largest together, however many tokens a row sees
+            const float fresh_at = fminf(fmaxf((float)(32 - __clz(seen)) - 15.f, 0.f), kFresh);
             float m = kNoMax, l = 0.f;
             bool has = false;
+#pragma unroll 1
             for (int k = pc.k0; k < pc.k1; ++k, ++j) {
                 if (RT == 1 && (j & 1) != g) continue;
-                const int q = RT == 2 ? 2 * j + g : j, b = q % NB;
-                const uint32_t s_tmem = tmem + b * 128 + lane_off;
+                const uint32_t s_tmem = tmem + g * 128 + lane_off;
+                const uint32_t p_tmem = SEP ? tmem + C::P_COL + g * 64 + lane_off : s_tmem;
                 if (!(ok = wwait(sc_full + 8 * (j % NSC), (uint32_t)(j / NSC) & 1))) break;
-                if (!(ok = wwait(s_full + 8 * b, (uint32_t)(q / NB) & 1))) break;
-                tc_fence_after();
                 const float4 *const sc = sc_sh + (j % NSC) * 8;
                 const int n0 = k * kTile;
                 const bool whole = __all_sync(0xffffffffu, n0 + kTile <= min_lim && sc[lane & 7].w != 0.f);
-                // the row's 128 products; hidden ones become -inf
-                uint32_t x[4][32];
-#pragma unroll
-                for (int c = 0; c < 4; ++c) tmem_ld32(s_tmem + 32 * c, x[c]);
-                tmem_wait_ld();
-                if (!whole) {
-#pragma unroll
-                    for (int c = 0; c < 4; ++c)
-#pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            if (n0 + 32 * c + i >= lim || sc[2 * c + (i >> 4)].w == 0.f) x[c][i] = 0xff800000u;
+                if (!(ok = wwait(s_full + 8 * g, (uint32_t)units & 1))) break;
+                tc_fence_after();
+                if (idle) {                                     // no row of this warp is anyone's
+                    if (SEP && lane == 0) mbar_arrive(s_free + 8 * g);
+                    if (lane == 0) mbar_arrive(p_full + 8 * g);
+                    has = true;
+                    ++units;
+                    continue;
                 }
-                // the largest exponent: a maximum of products in each page group, scaled once
-                // (the factors are positive)
-                float best = -INFINITY;
-#pragma unroll
-                for (int h = 0; h < 8; ++h) {
-                    const uint32_t *const y = &x[h >> 1][16 * (h & 1)];
-                    const float4 f = sc[h];
-                    float a0 = __uint_as_float(y[0]), a1 = __uint_as_float(y[1]);
-#pragma unroll
-                    for (int i = 2; i < 16; i += 4) {
-                        a0 = max3(a0, __uint_as_float(y[i]), __uint_as_float(y[i + 1]));
-                        if (i + 2 < 16) a1 = max3(a1, __uint_as_float(y[i + 2]), __uint_as_float(y[i + 3]));
-                    }
-                    best = fmaxf(best, fmaf(fmaxf(a0, a1), fac * f.x, f.y));
-                }
-                if (__any_sync(0xffffffffu, best > m + kHeadroom)) {
-                    // move the reference of the rows that need it
-                    const float nm = best > m + kHeadroom ? best - kFresh : m;
-                    const float f = ex2(m - nm);
-                    if (has) {
-                        if (!(ok = wwait(o_done + 8 * g, (uint32_t)(units - 1) & 1))) break;
-                        tc_fence_after();
+                uint32_t x[32];
+                // Rare: a tile with hidden tokens (their products become -inf where they lie), or
+                // rows that have seen no token yet (their reference is set from this tile).
+                const bool start = __any_sync(0xffffffffu, m == kNoMax && p.valid);
+                if (__builtin_expect(start || !whole, 0)) {
+                    float best = -INFINITY;
 #pragma unroll 1
-                        for (int c = 0; c < D / 32; ++c) {
-                            uint32_t o0[16], o1[16];
-                            tmem_ld16(o_tmem + c * 32, o0);
-                            tmem_ld16(o_tmem + c * 32 + 16, o1);
-                            tmem_wait_ld();
+                    for (int c = 0; c < 4; ++c) {
+                        tmem_ld32(s_tmem + 32 * c, x);
+                        tmem_wait_ld();
+                        float t[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-                            for (int i = 0; i < 16; ++i) {
-                                o0[i] = __float_as_uint(__uint_as_float(o0[i]) * f);
-                                o1[i] = __float_as_uint(__uint_as_float(o1[i]) * f);
-                            }
-                            tmem_st16(o_tmem + c * 32, o0);
-                            tmem_st16(o_tmem + c * 32 + 16, o1);
+                        for (int i = 0; i < 32; ++i) {
+                            if (n0 + 32 * c + i >= lim || sc[2 * c + (i >> 4)].w == 0.f) x[i] = 0xff800000u;
+                            t[i >> 4] = fmaxf(t[i >> 4], __uint_as_float(x[i]));
+                        }
+                        if (!whole) tmem_st32(s_tmem + 32 * c, x);
+                        // (the factors are positive: a page group's largest product is its largest score)
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            const float4 f = sc[2 * c + h];
+                            best = fmaxf(best, fmaf(t[h], fac * f.x, f.y));
                         }
                     }
-                    l *= f;
-                    m = nm;
+                    tmem_wait_st();
+                    if (m == kNoMax && best != -INFINITY) m = best - fresh_at;
                 }
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    uint32_t pw[16];
+                // The row's 128 products, 32 at a time: exponents against the reference as it is,
+                // the next products on their way, weights, their sums by page group. No pass for
+                // the maximum: a sum over kMaxSum (any weight that fp16 cannot hold makes one)
+                // sends the warp to the slow loop below with this and the following products.
+                float u[32], s[2];
+                uint32_t w[16];
+                auto exponents = [&](int c) {
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
                         const float4 f = sc[2 * c + h];
                         const float kc = fac * f.x, add = f.y - m;
                         const uint64_t kc2 = f2pack(kc, kc), ad2 = f2pack(add, add);
-                        uint64_t s2 = f2pack(0.f, 0.f);
+#pragma unroll
+                        for (int i = 16 * h; i < 16 * h + 16; i += 2)
+                            f2unpack(fma2(f2pack(__uint_as_float(x[i]), __uint_as_float(x[i + 1])), kc2, ad2), u[i], u[i + 1]);
+                    }
+                };
+                auto weights = [&]() {
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        uint64_t s2 = 0;
 #pragma unroll
                         for (int i = 0; i < 8; ++i) {
-                            float u0, u1;
-                            f2unpack(fma2(f2pack(__uint_as_float(x[c][16 * h + 2 * i]), __uint_as_float(x[c][16 * h + 2 * i + 1])), kc2, ad2), u0, u1);
-                            const float p0 = ex2(u0), p1 = ex2(u1);
-                            s2 = add2(s2, f2pack(p0, p1));
-                            pw[8 * h + i] = pack_f16(p0, p1);
+                            const float p0 = ex2(u[16 * h + 2 * i]), p1 = ex2(u[16 * h + 2 * i + 1]);
+                            s2 = i == 0 ? f2pack(p0, p1) : add2(s2, f2pack(p0, p1));
+                            w[8 * h + i] = pack_f16(p0, p1);
                         }
                         float s0, s1;
                         f2unpack(s2, s0, s1);
-                        l = fmaf(s0 + s1, f.z, l);
+                        s[h] = s0 + s1;
                     }
-                    tmem_st16(s_tmem + 16 * c, pw);
+                };
+                auto place = [&](int c) {
+                    l = fmaf(s[0], sc[2 * c].z, fmaf(s[1], sc[2 * c + 1].z, l));
+                    tmem_st16(p_tmem + 16 * c, w);
+                };
+                int from = 4;                                   // products that the slow loop takes
+                tmem_ld32(s_tmem, x);
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    tmem_wait_ld();
+                    exponents(c);
+                    if (c < 3) tmem_ld32(s_tmem + 32 * (c + 1), x);
+                    weights();
+                    // (w's own columns are free once the products of the unit before are done)
+                    if (SEP && c == 0 && has) ok = wwait(o_done + 8 * g, (uint32_t)(units - 1) & 1);
+                    if (__any_sync(0xffffffffu, fmaxf(s[0], s[1]) > kMaxSum)) {
+                        from = c;
+                        break;
+                    }
+                    place(c);
+                }
+                if (!ok) break;
+                if (__builtin_expect(from < 4, 0)) {
+                    if (has) {
+                        if (!(ok = wwait(o_done + 8 * g, (uint32_t)(units - 1) & 1))) break;
+                        tc_fence_after();
+                    }
+#pragma unroll 1
+                    for (int c = from; c < 4; ++c) {
+                        tmem_wait_ld();
+                        tmem_ld32(s_tmem + 32 * c, x);
+                        tmem_wait_ld();
+                        exponents(c);
+                        float top = u[0];
+#pragma unroll
+                        for (int i = 1; i < 32; ++i) top = fmaxf(top, u[i]);
+                        const bool over = top > kOver;
+                        if (__any_sync(0xffffffffu, over)) {
+                            // The references of the rows that need it move by whole powers of two:
+                            // O, l and the weights of this tile that are in place are scaled without
+                            // a rounding (but of what becomes subnormal).
+                            const float by = over ? ceilf(top) - fresh_at : 0.f;
+                            const float f = ex2(-by);
+                            const __half2 hf = __float2half2_rn(f);
+                            m += by;
+                            l *= f;
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) u[i] -= by;
+                            tmem_wait_st();
+#pragma unroll 1
+                            for (int d = 0; d < c; ++d) {
+                                tmem_ld16(p_tmem + 16 * d, w);
+                                tmem_wait_ld();
+#pragma unroll
+                                for (int i = 0; i < 16; ++i) {
+                                    const __half2 y = __hmul2(*reinterpret_cast<__half2 *>(&w[i]), hf);
+                                    w[i] = *reinterpret_cast<const uint32_t *>(&y);
+                                }
+                                tmem_st16(p_tmem + 16 * d, w);
+                            }
+                            if (has) {
+#pragma unroll 1
+                                for (int d = 0; d < D / 32; ++d) {
+                                    tmem_ld32(o_tmem + d * 32, x);
+                                    tmem_wait_ld();
+#pragma unroll
+                                    for (int i = 0; i < 32; ++i) x[i] = __float_as_uint(__uint_as_float(x[i]) * f);
+                                    tmem_st32(o_tmem + d * 32, x);
+                                }
+                            }
+                        }
+                        weights();
+                        place(c);
+                    }
+                }
+                if (SEP) {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(s_free + 8 * g);          // the scores may be overwritten
                 }
                 tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(p_full + 8 * b);
+                if (lane == 0) mbar_arrive(p_full + 8 * g);
                 has = true;
                 ++units;
             }
@@ -616,6 +701,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
             const float inv = !final ? 1.f : ls == 0.f ? 0.f : 1.f / ls;
             c0 *= inv;
             c1 *= inv;
+            const bool wide_o = !a.o_f32 && (reinterpret_cast<uintptr_t>(reinterpret_cast<__nv_bfloat16 *>(a.O) + p.o) & 15) == 0;
             // columns of this group: all of its own rows', or half of the shared rows'
             constexpr int NCOL = RT == 2 ? D : D / 2;
             const int col0 = RT == 2 ? 0 : g * (D / 2);
@@ -639,6 +725,12 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
                         for (int i = 0; i < 4; ++i)
                             *reinterpret_cast<float4 *>(&a.part_O[prow * D + col + 4 * i]) =
                                 make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+                    } else if (wide_o) {
+                        uint4 *o = reinterpret_cast<uint4 *>(reinterpret_cast<__nv_bfloat16 *>(a.O) + p.o + col);
+#pragma unroll
+                        for (int i = 0; i < 2; ++i)
+                            o[i] = make_uint4(pack_bf16(v[8 * i], v[8 * i + 1]), pack_bf16(v[8 * i + 2], v[8 * i + 3]),
+                                              pack_bf16(v[8 * i + 4], v[8 * i + 5]), pack_bf16(v[8 * i + 6], v[8 * i + 7]));
                     } else {
 #pragma unroll
                         for (int i = 0; i < 4; ++i)
@@ -686,11 +778,6 @@ cudaError_t launch_tc(const AttnArgs &a, cudaStream_t st) {
     auto k = attn_tc_kernel<D, RT>;
     cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::ALLOC);
     if (e != cudaSuccess) return e;
-    // the warpgroups' register budgets (setmaxnreg) must add up to no more
-    // than the block's registers at launch, or an increase would wait forever
-    cudaFuncAttributes fa;
-    if ((e = cudaFuncGetAttributes(&fa, k)) != cudaSuccess) return e;
-    if ((uint32_t)fa.numRegs * 4 < C::REG_CTL + C::REG_CVT + 2 * C::REG_SOFT) return cudaErrorInvalidConfiguration;
     k<<<a.grid, C::THREADS, C::ALLOC, st>>>(mk, mv, a);
     note_launch();
     return cudaGetLastError();

@@ -27,6 +27,8 @@ __device__ __forceinline__ Seq load_seq(const AttnArgs &a, int b) {
     return sequence(a.cu, a.n, a.T, a.lens, a.c.W * a.c.page, b);
 }
 
+// Everything below that is not called once a tile is kept out of line: inlined into every
+// role of a kernel it is more code than the instruction caches hold.
 // ---- span ------------------------------------------------------------------
 struct Cursor {
     int b, rt, h, k, nt, tiles_left;     // tile k of nt of the item; tiles of the span left
@@ -64,11 +66,12 @@ __device__ __forceinline__ int64_t block_scan(int64_t v, int64_t *sh, int64_t &t
 // block calls it; sh: NT / 32 int64, found: one Cursor, in shared memory.
 // An empty span leaves tiles_left = 0.
 template <int NT>
-__device__ __forceinline__ Span find_span(const AttnArgs &a, int c, int64_t *sh, Cursor *found) {
+static __device__ __noinline__ Span find_span(const AttnArgs &a, int c, int64_t *sh, Cursor *found) {
     const int tid = threadIdx.x, B = a.c.B;
     Span sp;
     sp.total = 0;
     int64_t first = 0;                   // this thread's tiles in the first block of sequences
+#pragma unroll 1
     for (int base = 0; base < B; base += NT) {
         int64_t v = 0, sum;
         if (base + tid < B) {
@@ -90,6 +93,7 @@ __device__ __forceinline__ Span find_span(const AttnArgs &a, int c, int64_t *sh,
     sp.begin = span_begin(sp.total, sp.parts, c);
     const int64_t end = span_begin(sp.total, sp.parts, c + 1);
     int64_t before = 0;
+#pragma unroll 1
     for (int base = 0; base < B; base += NT) {
         int64_t v = first, sum;
         if (base > 0) {
@@ -122,7 +126,7 @@ __device__ __forceinline__ Span find_span(const AttnArgs &a, int c, int64_t *sh,
 }
 
 // The next item after `cur` (called only while tiles of the span are left).
-__device__ __forceinline__ void next_item(const AttnArgs &a, Cursor &cur) {
+static __device__ __noinline__ void next_item(const AttnArgs &a, Cursor &cur) {
     cur.k = 0;
     if (++cur.h < a.c.H) return;
     cur.h = 0;
@@ -150,12 +154,12 @@ struct RowPlace {
     int limit;                           // tokens it sees
     int64_t q, o, l;                     // element offsets
 };
-__device__ __forceinline__ RowPlace row_place(const AttnArgs &a, const Seq &s, int b, int rt, int h, int row) {
+static __device__ __noinline__ RowPlace row_place(const AttnArgs &a, const Seq &s, int b, int rt, int h, int row) {
     RowPlace p;
-    const int64_t rr = (int64_t)rt * a.rows + row;
-    p.valid = rr < (int64_t)s.n * a.G;
-    const int i = p.valid ? (int)(rr / a.G) : 0;
-    const int hq = h * a.G + (p.valid ? (int)(rr - (int64_t)i * a.G) : 0);
+    const unsigned rr = (unsigned)rt * a.rows + row;            // rows of a head: under 2^31
+    p.valid = rr < (unsigned)(s.n * a.G);
+    const int i = p.valid ? (int)(rr / (unsigned)a.G) : 0;
+    const int hq = h * a.G + (p.valid ? (int)rr - i * a.G : 0);
     p.limit = p.valid ? limit_of(s, i, a.causal) : 0;
     p.q = (a.q_sb < 0 ? (s.t0 + i) * a.q_st : b * a.q_sb + i * a.q_st) + hq * a.q_sh;
     p.o = (a.o_sb < 0 ? (s.t0 + i) * a.o_st : b * a.o_sb + i * a.o_st) + hq * a.o_sh;
@@ -183,9 +187,17 @@ __device__ __forceinline__ float load_q(const AttnArgs &a, bool bf16, int64_t at
 __device__ __forceinline__ void store_o4(const AttnArgs &a, bool f32, int64_t at, float4 v) {
     if (f32) {
         float *o = reinterpret_cast<float *>(a.O) + at;
+        if ((reinterpret_cast<uintptr_t>(o) & 15) == 0) {
+            *reinterpret_cast<float4 *>(o) = v;
+            return;
+        }
         o[0] = v.x; o[1] = v.y; o[2] = v.z; o[3] = v.w;
     } else {
         __nv_bfloat16 *o = reinterpret_cast<__nv_bfloat16 *>(a.O) + at;
+        if ((reinterpret_cast<uintptr_t>(o) & 7) == 0) {
+            *reinterpret_cast<uint2 *>(o) = make_uint2(tc::pack_bf16(v.x, v.y), tc::pack_bf16(v.z, v.w));
+            return;
+        }
         o[0] = __float2bfloat16_rn(v.x); o[1] = __float2bfloat16_rn(v.y);
         o[2] = __float2bfloat16_rn(v.z); o[3] = __float2bfloat16_rn(v.w);
     }

@@ -55,32 +55,33 @@ FLARE_HD Seq sequence(const int32_t *cu, int n, int64_t T, const int32_t *lens, 
 // Row r of a sequence and shared head is query token r / G, query head
 // h * G + r % G. Rows are taken `rows` at a time (row tiles); a row tile sees
 // the tokens [0, visible()) at most.
+// (rows of a sequence and head: under 2^31 - 256)
 FLARE_HD int row_tiles(const Seq &s, int G, int rows) {
-    return (int)(((int64_t)s.n * G + rows - 1) / rows);
+    return (int)(((unsigned)(s.n * G) + rows - 1) / (unsigned)rows);
 }
 FLARE_HD int visible(const Seq &s, int G, int rows, int rt, bool causal) {
     if (!causal) return s.len;
-    const int64_t last = ((int64_t)(rt + 1) * rows - 1) / G;      // last query token of the tile
-    const int64_t i = lmin(last, s.n - 1);
-    const int64_t seen = (int64_t)s.len - s.n + i + 1;
-    return (int)(seen < 0 ? 0 : seen);
+    const int last = (int)(((unsigned)(rt + 1) * rows - 1) / (unsigned)G);      // last query token of the tile
+    return imax(0, s.len - s.n + imin(last, s.n - 1) + 1);
 }
 // Tokens that query token i sees.
 FLARE_HD int limit_of(const Seq &s, int i, bool causal) {
     if (!causal) return s.len;
-    const int64_t seen = (int64_t)s.len - s.n + i + 1;
-    return (int)(seen < 0 ? 0 : seen);
+    return imax(0, s.len - s.n + i + 1);
 }
 // Tiles of one (row tile, head): one at least, so that somebody writes the
 // rows that see nothing.
 FLARE_HD int item_tiles(const Seq &s, int G, int rows, int rt, bool causal) {
-    return imax(1, (visible(s, G, rows, rt, causal) + kTile - 1) / kTile);
+    return imax(1, (int)((unsigned)(visible(s, G, rows, rt, causal) + kTile - 1) / kTile));
 }
 // Tiles of one head over the row tiles of a sequence.
 FLARE_HD int64_t seq_tiles(const Seq &s, int G, int rows, bool causal) {
     const int m = row_tiles(s, G, rows);
     if (!causal) return m > 0 ? (int64_t)m * item_tiles(s, G, rows, 0, false) : 0;
     int64_t sum = 0;
+#ifdef __CUDACC__
+#pragma unroll 1
+#endif
     for (int rt = 0; rt < m; ++rt) sum += item_tiles(s, G, rows, rt, true);
     return sum;
 }
