@@ -182,6 +182,7 @@ flare_status_t append_run(const flare_cache_dims_t *d, const flare_cache_t *cach
     a.inv_freq = inv_freq;
     a.rot = inv_freq ? rot : 0;
     a.inter = interleaved != 0;
+    a.per = 0;
     a.lens_out = lens_out;
     int sms;
     if ((s = device_facts(&sms, &a.status)) != FLARE_OK) return s;

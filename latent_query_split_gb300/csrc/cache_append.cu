@@ -75,45 +75,32 @@ __device__ __forceinline__ float rotated(const AppendArgs &a, const void *x, int
 }
 
 struct Slot {
-    Seq s;
-    int b, page, off, count, pos;        // page of the pool, first slot, new tokens, first position
+    int b, page, off, count, pos;        // sequence, page of the pool, first slot, new tokens, first position
     int64_t t;                           // first token row
 };
 
-__device__ __forceinline__ uint8_t e4m3_of(float x) {
-    return (uint8_t)__nv_cvt_float_to_fp8(x, __NV_SATFINITE, __NV_E4M3);
-}
-__device__ __forceinline__ float float_of(uint8_t c) {
-    return __half2float(__half(__nv_cvt_fp8_to_halfraw(c, __NV_E4M3)));
-}
-
-// One block a touched page and head: the largest new magnitude, the scale, the
-// old codes if it grew, the new codes; keys, then values.
-template <bool BF16>
-__global__ void __launch_bounds__(256) append_kernel(const AppendArgs a) {
-    __shared__ Slot sl;
-    __shared__ float amax_sh[8];
-    __shared__ uint32_t bad_sh[4];       // tokens of the page with a non-finite channel
-    const int tid = threadIdx.x, D = a.c.D, page = a.c.page, B = a.c.B;
-    const int64_t slot = blockIdx.x;
-    const int capacity = a.c.W * page;
+// The touched page that block column blockIdx.x is for (b = -1: none). One block
+// of the grid also writes the lengths after the call.
+__device__ __forceinline__ void find_slot(const AppendArgs &a, Slot &sl) {
+    const int tid = threadIdx.x, page = a.c.page, capacity = a.c.W * page;
+    const bool first_block = blockIdx.x == 0 && blockIdx.y == 0;
     if (tid == 0) sl.b = -1;
-    if (tid < 4) bad_sh[tid] = 0;
     __syncthreads();
-    for (int b = tid; b < B; b += 256) {
+    // equal sequences: a.per pages each at most; else the numbers of first_slot()
+    const int only = a.per ? (int)(blockIdx.x / a.per) : -1;
+    const int lo = a.per && !first_block ? only : 0, hi = a.per && !first_block ? only + 1 : a.c.B;
+    for (int b = lo + tid; b < hi; b += blockDim.x) {
         const Seq s = sequence(a.cu, a.n, a.T, a.lens, capacity, b);
-        const int64_t first = first_slot(s.t0, b, page);
         const int n = imin(s.n, capacity - s.len);           // what the table has room for
-        if (slot == 0 && blockIdx.y == 0) {
+        if (first_block) {
             if (!s.ok || n < s.n) atomicCAS(a.status, 0u, (unsigned)kDevBadCache);
             if (a.lens_out) a.lens_out[b] = s.len + n;
         }
-        const int i = (int)(slot - first);
-        if (slot >= first && i < touched_pages(s.len, n, page)) {
+        const int64_t i = a.per ? (b == only ? (int64_t)(blockIdx.x % a.per) : -1) : (int64_t)blockIdx.x - first_slot(s.t0, b, page);
+        if (i >= 0 && i < touched_pages(s.len, n, page)) {
             Slot x;
-            x.s = s;
             x.b = b;
-            const int at = s.len / page + i;
+            const int at = s.len / page + (int)i;
             x.page = a.c.table[(int64_t)b * a.c.W + at];
             x.off = i == 0 ? s.len % page : 0;
             x.pos = at * page + x.off;
@@ -128,6 +115,408 @@ __global__ void __launch_bounds__(256) append_kernel(const AppendArgs a) {
         }
     }
     __syncthreads();
+}
+
+__device__ __forceinline__ uint8_t e4m3_of(float x) {
+    return (uint8_t)__nv_cvt_float_to_fp8(x, __NV_SATFINITE, __NV_E4M3);
+}
+__device__ __forceinline__ float float_of(uint8_t c) {
+    return __half2float(__half(__nv_cvt_fp8_to_halfraw(c, __NV_E4M3)));
+}
+
+// ---- tasks: 16 channels of a token ---------------------------------------------------
+// Two runs of 8 channels, at `a` and `b`, so that both channels of a rotated pair
+// are one thread's: of halves, (a + i, b + i); side by side, (2i, 2i + 1) of each
+// run. Pair i of the task turns by inv_freq[8 p + i].
+struct Task {
+    int t, p, a, b;                      // token of the page, task of the token, the runs
+    bool turned;
+    float c[8], s[8];
+};
+template <bool INTER>
+__device__ __forceinline__ void make_task(const AppendArgs &a, const Slot &x, int id, Task &k, const uint64_t *freq) {
+    const int per = a.c.D >> 4;
+    k.t = id / per;
+    k.p = id - k.t * per;
+    k.turned = 16 * k.p < a.rot;
+    k.a = !INTER && k.turned ? 8 * k.p : 16 * k.p;
+    k.b = !INTER && k.turned ? a.rot / 2 + 8 * k.p : 16 * k.p + 8;
+    if (k.turned)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) sincos_at(x.pos + k.t, freq[8 * k.p + i], k.s[i], k.c[i]);
+}
+// 8 channels, as loaded.
+template <bool BF16>
+struct Raw;
+template <>
+struct Raw<true> {
+    uint4 v;
+    __device__ __forceinline__ void load(const void *p, int64_t i) {
+        v = *reinterpret_cast<const uint4 *>(reinterpret_cast<const __nv_bfloat16 *>(p) + i);
+    }
+    __device__ __forceinline__ void zero() { v = make_uint4(0, 0, 0, 0); }
+    __device__ __forceinline__ void get(float (&x)[8]) const {
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            x[2 * i] = __uint_as_float(w[i] << 16);
+            x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+        }
+    }
+    // the bits of the largest magnitude: those of inf and NaN are above all others
+    __device__ __forceinline__ uint32_t top() const {
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+        uint32_t m = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) m = max(m, max(w[i] & 0x7fff0000u, (w[i] << 16) & 0x7fff0000u));
+        return m;
+    }
+    static __device__ __forceinline__ void store(void *p, int64_t i, const float (&x)[8]) {
+        uint32_t w[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const __nv_bfloat162 y = __floats2bfloat162_rn(x[2 * k], x[2 * k + 1]);
+            w[k] = *reinterpret_cast<const uint32_t *>(&y);
+        }
+        *reinterpret_cast<uint4 *>(reinterpret_cast<__nv_bfloat16 *>(p) + i) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+};
+template <>
+struct Raw<false> {
+    float4 u, v;
+    __device__ __forceinline__ void load(const void *p, int64_t i) {
+        const float4 *q = reinterpret_cast<const float4 *>(reinterpret_cast<const float *>(p) + i);
+        u = q[0];
+        v = q[1];
+    }
+    __device__ __forceinline__ void zero() { u = v = make_float4(0.f, 0.f, 0.f, 0.f); }
+    __device__ __forceinline__ void get(float (&x)[8]) const {
+        x[0] = u.x; x[1] = u.y; x[2] = u.z; x[3] = u.w;
+        x[4] = v.x; x[5] = v.y; x[6] = v.z; x[7] = v.w;
+    }
+    __device__ __forceinline__ uint32_t top() const {
+        float x[8];
+        get(x);
+        uint32_t m = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(x[i]) & 0x7fffffffu);
+        return m;
+    }
+    static __device__ __forceinline__ void store(void *p, int64_t i, const float (&x)[8]) {
+        float4 *q = reinterpret_cast<float4 *>(reinterpret_cast<float *>(p) + i);
+        q[0] = make_float4(x[0], x[1], x[2], x[3]);
+        q[1] = make_float4(x[4], x[5], x[6], x[7]);
+    }
+};
+template <bool INTER>
+__device__ __forceinline__ void rotate(const Task &k, float (&x)[8], float (&y)[8]) {
+    if (!k.turned) return;
+    if (INTER) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float a = x[2 * i], b = x[2 * i + 1], c = y[2 * i], d = y[2 * i + 1];
+            x[2 * i] = a * k.c[i] - b * k.s[i];
+            x[2 * i + 1] = a * k.s[i] + b * k.c[i];
+            y[2 * i] = c * k.c[4 + i] - d * k.s[4 + i];
+            y[2 * i + 1] = c * k.s[4 + i] + d * k.c[4 + i];
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float a = x[i], b = y[i];
+            x[i] = a * k.c[i] - b * k.s[i];
+            y[i] = a * k.s[i] + b * k.c[i];
+        }
+    }
+}
+__device__ __forceinline__ uint32_t pack4(float a, float b, float c, float d) {
+    uint16_t lo, hi;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(b), "f"(a));
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(d), "f"(c));
+    return (uint32_t)lo | (uint32_t)hi << 16;
+}
+__device__ __forceinline__ void store_codes(uint8_t *p, const float (&x)[8], float inv) {
+    *reinterpret_cast<uint2 *>(p) = make_uint2(pack4(x[0] * inv, x[1] * inv, x[2] * inv, x[3] * inv),
+                                               pack4(x[4] * inv, x[5] * inv, x[6] * inv, x[7] * inv));
+}
+// The codes of `bytes` (a multiple of 16) earlier channels times 2^by, by < 0.
+__device__ __forceinline__ void rescale(uint8_t *codes, int bytes, int by, int i0, int step) {
+    const float f = two_to(by);
+    for (int i = 16 * i0; i < bytes; i += 16 * step) {
+        const uint4 v = *reinterpret_cast<const uint4 *>(codes + i);
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+        uint32_t o[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            o[k] = pack4(float_of(w[k] & 0xff) * f, float_of(w[k] >> 8 & 0xff) * f, float_of(w[k] >> 16 & 0xff) * f,
+                         float_of(w[k] >> 24) * f);
+        *reinterpret_cast<uint4 *>(codes + i) = make_uint4(o[0], o[1], o[2], o[3]);
+    }
+}
+// Largest finite magnitude of 8 channels; *bad where one is not finite.
+template <bool BF16>
+__device__ __forceinline__ uint32_t finite_top(const Raw<BF16> &r, bool &bad) {
+    float x[8];
+    r.get(x);
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const uint32_t u = __float_as_uint(x[i]) & 0x7fffffffu;
+        if (u < 0x7f800000u) m = max(m, u);
+        else bad = true;
+    }
+    return m;
+}
+
+// ---- prompts: one block a touched page and some heads ------------------------------
+// THR threads (whole warps) share a head's tile of the page, all its tokens in
+// registers: the largest magnitude over them, then the codes; keys and values of a
+// head together. Each thread has the same TPT tasks of every head, so its angles
+// are computed once for the block's heads. Queries have no scale: they stream.
+// Bound by memory: each token is read once and written once. One pass with the
+// tile in registers reads half of what a pass for the scale and one for the codes
+// would. 24,213 tokens with 8 cache and 32 query heads of 128 (529 MB): see the
+// launcher.
+template <bool BF16, bool INTER, int TPT>
+__global__ void __launch_bounds__(256) append_page_kernel(const AppendArgs a, const int thr, const int kv_parts,
+                                                          const int kv_heads, const int q_heads) {
+    __shared__ Slot sl;
+    __shared__ uint64_t freq[64];
+    __shared__ uint32_t red[2][8][2];
+    __shared__ uint32_t bad_sh[8][4];                // by group: tokens with a channel that is not finite
+    const int tid = threadIdx.x, D = a.c.D, page = a.c.page, H = a.c.H;
+    if (tid < a.rot / 2) freq[tid] = turns_of(a.inv_freq[tid]);
+    find_slot(a, sl);
+    if (sl.b < 0) return;
+    const Slot x = sl;
+    const int tasks = x.count * (D >> 4);
+    const bool keys = (int)blockIdx.y < kv_parts;
+    const int groups = 256 / thr, group = tid / thr, lane_in = tid - group * thr;
+    Task k[TPT];
+    bool on[TPT];
+#pragma unroll
+    for (int i = 0; i < TPT; ++i) {
+        const int id = lane_in + i * thr;
+        on[i] = group < groups && id < tasks;
+        k[i].turned = false;
+        if (on[i]) make_task<INTER>(a, x, id, k[i], freq);
+    }
+    if (!keys) {
+        const int h0 = ((int)blockIdx.y - kv_parts) * q_heads, h1 = imin(a.Hq, h0 + q_heads);
+        for (int h = h0 + group; h < h1; h += groups) {
+            Raw<BF16> r[TPT][2];
+#pragma unroll
+            for (int i = 0; i < TPT; ++i)
+                if (on[i]) {
+                    const int64_t row = (x.t + k[i].t) * a.q_st + (int64_t)h * D;
+                    r[i][0].load(a.Q, row + k[i].a);
+                    r[i][1].load(a.Q, row + k[i].b);
+                }
+#pragma unroll
+            for (int i = 0; i < TPT; ++i)
+                if (on[i]) {
+                    float u[8], v[8];
+                    r[i][0].get(u);
+                    r[i][1].get(v);
+                    rotate<INTER>(k[i], u, v);
+                    const int64_t o = ((x.t + k[i].t) * a.Hq + h) * D;
+                    Raw<BF16>::store(a.Q_out, o + k[i].a, u);
+                    Raw<BF16>::store(a.Q_out, o + k[i].b, v);
+                }
+        }
+        return;
+    }
+    const int h0 = (int)blockIdx.y * kv_heads, h1 = imin(H, h0 + kv_heads);
+    int parity = 0;
+    for (int base = h0; base < h1; base += groups, parity ^= 1) {
+        const int h = base + group;
+        const bool live = group < groups && h < h1;
+        const int64_t ph = (int64_t)x.page * H + h;
+        Raw<BF16> r[2][TPT][2];
+        int was[2] = {kEMin, kEMin};
+        uint32_t top[2] = {0, 0};
+        if (live) {
+#pragma unroll
+            for (int kv = 0; kv < 2; ++kv) {
+                const void *src = kv ? a.V : a.K;
+                const int64_t st = kv ? a.v_st : a.k_st;
+#pragma unroll
+                for (int i = 0; i < TPT; ++i) {
+                    r[kv][i][0].zero();
+                    r[kv][i][1].zero();
+                    if (on[i]) {
+                        const int64_t row = (x.t + k[i].t) * st + (int64_t)h * D;
+                        r[kv][i][0].load(src, row + k[i].a);
+                        r[kv][i][1].load(src, row + k[i].b);
+                    }
+                }
+                if (x.off) was[kv] = exponent_in((kv ? a.c.vs : a.c.ks)[ph]);
+            }
+#pragma unroll
+            for (int kv = 0; kv < 2; ++kv)
+#pragma unroll
+                for (int i = 0; i < TPT; ++i) top[kv] = max(top[kv], max(r[kv][i][0].top(), r[kv][i][1].top()));
+        }
+        auto reduce = [&]() {
+#pragma unroll
+            for (int kv = 0; kv < 2; ++kv) {
+                top[kv] = __reduce_max_sync(0xffffffffu, top[kv]);
+                if ((tid & 31) == 0) red[parity][tid >> 5][kv] = top[kv];
+            }
+            __syncthreads();
+            for (int w = group * (thr >> 5); w < imin(8, (group + 1) * (thr >> 5)); ++w) {
+                top[0] = max(top[0], red[parity][w][0]);
+                top[1] = max(top[1], red[parity][w][1]);
+            }
+        };
+        reduce();
+        bool marked = false;
+        if (__syncthreads_or(max(top[0], top[1]) >= 0x7f800000u)) {
+            // rare: a channel that is not finite. Its token is held as a NaN key and a zero
+            // value, and has no part in the scale.
+            if (lane_in < 4 && group < groups) bad_sh[group][lane_in] = 0;
+            __syncthreads();
+            top[0] = top[1] = 0;
+            if (live)
+#pragma unroll
+                for (int kv = 0; kv < 2; ++kv)
+#pragma unroll
+                    for (int i = 0; i < TPT; ++i)
+                        if (on[i]) {
+                            bool bad = false;
+                            top[kv] = max(top[kv], max(finite_top<BF16>(r[kv][i][0], bad), finite_top<BF16>(r[kv][i][1], bad)));
+                            if (bad) atomicOr(&bad_sh[group][k[i].t >> 5], 1u << (k[i].t & 31));
+                        }
+            __syncthreads();
+            reduce();
+            marked = true;
+        }
+        if (live) {
+#pragma unroll
+            for (int kv = 0; kv < 2; ++kv) {
+                const int e = imax(was[kv], exponent_of(__uint_as_float(top[kv])));
+                uint8_t *codes = (kv ? a.c.v : a.c.k) + ph * page * D;
+                if (lane_in == 0) (kv ? a.c.vs : a.c.ks)[ph] = two_to(e);
+                if (x.off && e > was[kv]) rescale(codes, x.off * D, was[kv] - e, lane_in, thr);
+                const float inv = two_to(-e);
+#pragma unroll
+                for (int i = 0; i < TPT; ++i)
+                    if (on[i]) {
+                        float u[8], v[8];
+                        r[kv][i][0].get(u);
+                        r[kv][i][1].get(v);
+                        if (!kv) rotate<INTER>(k[i], u, v);
+                        if (marked && (bad_sh[group][k[i].t >> 5] >> (k[i].t & 31) & 1))
+#pragma unroll
+                            for (int y = 0; y < 8; ++y) u[y] = v[y] = kv ? 0.f : NAN;
+                        uint8_t *o = codes + (x.off + k[i].t) * D;
+                        store_codes(o + k[i].a, u, inv);
+                        store_codes(o + k[i].b, v, inv);
+                    }
+            }
+        }
+    }
+}
+
+// ---- a token or a few a sequence: one warp a touched page and head ------------------
+// What counts is latency: a warp reads its head's keys and values once for the
+// scale and once (from the caches) for the codes. Eight query heads are one warp's.
+constexpr int kQHeads = 8;
+template <bool BF16, bool INTER>
+__global__ void __launch_bounds__(256) append_token_kernel(const AppendArgs a) {
+    __shared__ Slot sl;
+    __shared__ uint64_t freq[64];
+    const int tid = threadIdx.x, lane = tid & 31, D = a.c.D, page = a.c.page, H = a.c.H, per = D >> 4;
+    if (tid < a.rot / 2) freq[tid] = turns_of(a.inv_freq[tid]);
+    find_slot(a, sl);
+    if (sl.b < 0) return;
+    const Slot x = sl;
+    int item = (int)blockIdx.y * 8 + (tid >> 5);
+    if (item >= H) {
+        item -= H;
+        const int h0 = item * kQHeads, heads = imin(a.Hq, h0 + kQHeads) - h0;
+        for (int i = lane; i < x.count * per; i += 32) {
+            Task k;
+            k.turned = false;
+            make_task<INTER>(a, x, i, k, freq);
+            for (int h = h0; h < h0 + heads; ++h) {
+                Raw<BF16> r[2];
+                const int64_t row = (x.t + k.t) * a.q_st + (int64_t)h * D, o = ((x.t + k.t) * a.Hq + h) * D;
+                r[0].load(a.Q, row + k.a);
+                r[1].load(a.Q, row + k.b);
+                float u[8], v[8];
+                r[0].get(u);
+                r[1].get(v);
+                rotate<INTER>(k, u, v);
+                Raw<BF16>::store(a.Q_out, o + k.a, u);
+                Raw<BF16>::store(a.Q_out, o + k.b, v);
+            }
+        }
+        return;
+    }
+    const int h = item;
+    const int64_t ph = (int64_t)x.page * H + h;
+    uint32_t top[2] = {0, 0};
+    const int was[2] = {x.off ? exponent_in(a.c.ks[ph]) : kEMin, x.off ? exponent_in(a.c.vs[ph]) : kEMin};
+    bool bad = false;
+    for (int i = lane; i < 2 * x.count * per; i += 32) {
+        const int id = i >> 1, t = id / per, p = id - t * per;
+#pragma unroll
+        for (int kv = 0; kv < 2; ++kv) {
+            Raw<BF16> r;
+            r.load(kv ? a.V : a.K, (x.t + t) * (kv ? a.v_st : a.k_st) + (int64_t)h * D + 16 * p + 8 * (i & 1));
+            top[kv] = max(top[kv], finite_top<BF16>(r, bad));
+        }
+    }
+    const bool any_bad = __any_sync(0xffffffffu, bad);
+    int e[2];
+#pragma unroll
+    for (int kv = 0; kv < 2; ++kv) {
+        e[kv] = imax(was[kv], exponent_of(__uint_as_float(__reduce_max_sync(0xffffffffu, top[kv]))));
+        if (lane == 0) (kv ? a.c.vs : a.c.ks)[ph] = two_to(e[kv]);
+        if (x.off && e[kv] > was[kv])
+            rescale((kv ? a.c.v : a.c.k) + ph * page * D, x.off * D, was[kv] - e[kv], lane, 32);
+    }
+    for (int i = lane; i < x.count * per; i += 32) {
+        Task k;
+        k.turned = false;
+        make_task<INTER>(a, x, i, k, freq);
+        bool lost = false;
+        if (any_bad)
+            for (int d = 0; d < D; ++d)
+                lost = lost || !finite(load1<BF16>(a.K, (x.t + k.t) * a.k_st + (int64_t)h * D + d)) ||
+                       !finite(load1<BF16>(a.V, (x.t + k.t) * a.v_st + (int64_t)h * D + d));
+#pragma unroll
+        for (int kv = 0; kv < 2; ++kv) {
+            Raw<BF16> r[2];
+            const int64_t row = (x.t + k.t) * (kv ? a.v_st : a.k_st) + (int64_t)h * D;
+            r[0].load(kv ? a.V : a.K, row + k.a);
+            r[1].load(kv ? a.V : a.K, row + k.b);
+            float u[8], v[8];
+            r[0].get(u);
+            r[1].get(v);
+            if (!kv) rotate<INTER>(k, u, v);
+            if (lost)
+#pragma unroll
+                for (int y = 0; y < 8; ++y) u[y] = v[y] = kv ? 0.f : NAN;
+            uint8_t *o = (kv ? a.c.v : a.c.k) + (ph * page + x.off + k.t) * D;
+            store_codes(o + k.a, u, two_to(-e[kv]));
+            store_codes(o + k.b, v, two_to(-e[kv]));
+        }
+    }
+}
+
+// ---- any alignment, any even number of rotated channels -----------------------------
+// One block a touched page and head: the largest new magnitude, the scale, the
+// old codes if it grew, the new codes; keys, then values.
+template <bool BF16>
+__global__ void __launch_bounds__(256) append_kernel(const AppendArgs a) {
+    __shared__ Slot sl;
+    __shared__ float amax_sh[8];
+    __shared__ uint32_t bad_sh[4];       // tokens of the page with a non-finite channel
+    const int tid = threadIdx.x, D = a.c.D, page = a.c.page;
+    if (tid < 4) bad_sh[tid] = 0;
+    find_slot(a, sl);
     if (sl.b < 0) return;
     const int h = blockIdx.y;
     const Slot x = sl;
@@ -190,14 +579,59 @@ __global__ void __launch_bounds__(256) append_kernel(const AppendArgs a) {
     }
 }
 
+template <bool BF16, bool INTER>
+void launch_pages(const AppendArgs &a, unsigned slots, int thr, int tpt, cudaStream_t st) {
+    // as many heads a block as leave a few blocks a multiprocessor: the angles are per block
+    const int groups = 256 / thr;
+    int kv = 8, q = 16;
+    while (kv > groups && (int64_t)slots * ((a.c.H + kv - 1) / kv + (a.Hq + q - 1) / q) < 1200) {
+        kv /= 2;
+        q /= 2;
+    }
+    const int kv_parts = (a.c.H + kv - 1) / kv, q_parts = a.Q ? (a.Hq + q - 1) / q : 0;
+    const dim3 grid(slots, kv_parts + q_parts);
+    if (tpt == 1) append_page_kernel<BF16, INTER, 1><<<grid, 256, 0, st>>>(a, thr, kv_parts, kv, q);
+    else if (tpt == 2) append_page_kernel<BF16, INTER, 2><<<grid, 256, 0, st>>>(a, thr, kv_parts, kv, q);
+    else append_page_kernel<BF16, INTER, 4><<<grid, 256, 0, st>>>(a, thr, kv_parts, kv, q);
+}
+
 }  // namespace
 
-cudaError_t launch_append(const AppendArgs &a, bool bf16, cudaStream_t st) {
-    const dim3 grid((unsigned)slot_bound(a.T, a.c.B, a.c.page), a.c.H + (a.Q ? a.Hq : 0));
-    if (bf16)
-        append_kernel<true><<<grid, 256, 0, st>>>(a);
-    else
-        append_kernel<false><<<grid, 256, 0, st>>>(a);
+cudaError_t launch_append(const AppendArgs &args, bool bf16, cudaStream_t st) {
+    AppendArgs a = args;
+    const int page = a.c.page, es = bf16 ? 2 : 4;
+    // equal sequences of n tokens touch no more than this many pages each
+    a.per = a.cu || a.T == 0 ? 0 : a.n < 2 ? 1 : (a.n - 2) / page + 2;
+    if (!a.Q) a.Hq = 0;
+    const int64_t slots = a.per ? (int64_t)a.per * a.c.B : slot_bound(a.T, a.c.B, page);
+    auto fits = [&](const void *p, int64_t stride) { return (uintptr_t)p % 16 == 0 && stride * es % 16 == 0; };
+    const bool fast = fits(a.K, a.k_st) && fits(a.V, a.v_st) && fits(a.Q, a.q_st) && fits(a.Q_out, 0) && a.rot % 16 == 0;
+    if (!fast) {
+        const dim3 grid((unsigned)slots, a.c.H + a.Hq);
+        if (bf16)
+            append_kernel<true><<<grid, 256, 0, st>>>(a);
+        else
+            append_kernel<false><<<grid, 256, 0, st>>>(a);
+    } else if (a.T <= 8 * (int64_t)a.c.B) {
+        const dim3 grid((unsigned)slots, (a.c.H + (a.Hq + kQHeads - 1) / kQHeads + 7) / 8);
+        if (bf16) {
+            if (a.inter) append_token_kernel<true, true><<<grid, 256, 0, st>>>(a);
+            else append_token_kernel<true, false><<<grid, 256, 0, st>>>(a);
+        } else {
+            if (a.inter) append_token_kernel<false, true><<<grid, 256, 0, st>>>(a);
+            else append_token_kernel<false, false><<<grid, 256, 0, st>>>(a);
+        }
+    } else {
+        const int tasks = page * (a.c.D / 16), thr = tasks >= 256 ? 256 : (tasks + 31) / 32 * 32;
+        const int tpt = (tasks + thr - 1) / thr, up = tpt > 2 ? 4 : tpt;
+        if (bf16) {
+            if (a.inter) launch_pages<true, true>(a, (unsigned)slots, thr, up, st);
+            else launch_pages<true, false>(a, (unsigned)slots, thr, up, st);
+        } else {
+            if (a.inter) launch_pages<false, true>(a, (unsigned)slots, thr, up, st);
+            else launch_pages<false, false>(a, (unsigned)slots, thr, up, st);
+        }
+    }
     note_launch();
     return cudaGetLastError();
 }

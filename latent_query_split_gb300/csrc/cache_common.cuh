@@ -55,6 +55,7 @@ struct AppendArgs {
     int64_t T;
     const float *inv_freq;
     int rot, inter;
+    int per;                            // pages that each of equal sequences may touch (0: ragged)
     int32_t *lens_out;
     unsigned *status;
 };
