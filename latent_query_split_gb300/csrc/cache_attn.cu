@@ -231,7 +231,7 @@ AttnPlan attn_plan(const Pool &c, int G, bool bf16, int64_t T, int family, int s
     p.rows = p.kernel == AttnKernel::kSimt ? 8 : p.kernel == AttnKernel::kTc ? (per_seq > 128 ? 256 : 128)
              : bf16 && per_seq > 16        ? 32
                                            : 16;
-    int64_t grid = (int64_t)sms * (p.kernel == AttnKernel::kSimt ? 4 : 1);
+    int64_t grid = (int64_t)sms * (p.kernel == AttnKernel::kSimt ? 4 : p.kernel == AttnKernel::kMma ? 2 : 1);
     // no more spans than there can be tiles
     const int64_t tiles = ((T * G + p.rows - 1) / p.rows + c.B) * c.H *
                           (((int64_t)c.W * c.page + kTile - 1) / kTile + 1);

@@ -86,7 +86,9 @@ __device__ __forceinline__ uint32_t pack_rest(float lo, float hi, uint32_t kept)
 
 template <int DP, int MT, bool F32>
 struct MmaCfg {
-    static constexpr int NW = 8, NT = 32 * NW;
+    // two blocks a multiprocessor: one's loads run while the other joins its warps, writes and
+    // begins its next piece
+    static constexpr int NW = MT == 1 && !F32 ? 6 : 4, NT = 32 * NW;
     static constexpr int ROWS = 16 * MT;
     static constexpr int KJ = DP / 64;                    // 16-byte chunks of a key row a lane holds
     static constexpr int KS = DP / 16;                    // k-steps of S
@@ -94,7 +96,7 @@ struct MmaCfg {
     static constexpr int PARTS = F32 ? 2 : 1;
     static constexpr int VB = DP / 8;                     // bytes of a value row a lane holds
     static constexpr uint32_t UNIT = 32 * (2 * KJ * 16 + 4 * VB) + 256;   // codes, then the scales
-    static constexpr int STAGES = DP == 128 ? 5 : 8;
+    static constexpr int STAGES = DP == 128 ? (NW == 6 ? 4 : 5) : 8;
     static constexpr uint32_t RING = NW * STAGES * UNIT;
     static constexpr uint32_t OS = DP + 8;                // padded row of the joining buffer
     static constexpr uint32_t JOIN = NW * ROWS * OS * 4;
@@ -102,11 +104,11 @@ struct MmaCfg {
     static constexpr uint32_t Q_BYTES = MT * PARTS * KS * 512;
     static constexpr uint32_t ML_OFF = Q_OFF + Q_BYTES;   // m, l of each warp and row; row factors
     static constexpr uint32_t BYTES = ML_OFF + 2 * NW * ROWS * 4 + ROWS * 4;
-    static_assert(BYTES <= 232448 - 1024, "shared memory of one CTA exceeded");
+    static_assert(2 * (BYTES + 1024 + 512) <= 233472, "shared memory of two CTAs exceeded");
 };
 
 template <int DP, int MT, bool F32>
-__global__ void __launch_bounds__(MmaCfg<DP, MT, F32>::NT, 1) attn_mma_kernel(const AttnArgs a) {
+__global__ void __launch_bounds__(MmaCfg<DP, MT, F32>::NT, 2) attn_mma_kernel(const AttnArgs a) {
     using C = MmaCfg<DP, MT, F32>;
     constexpr int NW = C::NW, NT = C::NT, ROWS = C::ROWS, KJ = C::KJ, KS = C::KS, NO = C::NO, STAGES = C::STAGES;
     extern __shared__ __align__(128) uint8_t smem[];
@@ -116,6 +118,10 @@ __global__ void __launch_bounds__(MmaCfg<DP, MT, F32>::NT, 1) attn_mma_kernel(co
     const int g = lane >> 2, t = lane & 3;
     const int D = a.c.D, page_log2 = a.c.page_log2, H = a.c.H;
     const uint32_t sbase = tc::smem_u32(smem);
+    const int k_off = g * DP + 16 * t, v_off = 2 * t * DP + C::VB * g;      // this lane's first bytes (D = DP)
+    // where a lane's bytes of a value row lie: the row's together, in an order in which neither
+    // the copies of a row nor the lanes of a load meet in a bank
+    const uint32_t v_slot = (8 * t + (DP == 128 ? g ^ (2 * t) : g ^ (4 * (t >> 1)))) * C::VB;
     const uint32_t ring = sbase + (uint32_t)w * STAGES * C::UNIT;
     float *const join = reinterpret_cast<float *>(smem);
     float *const m_sh = reinterpret_cast<float *>(smem + C::ML_OFF), *const l_sh = m_sh + NW * ROWS;
@@ -154,27 +160,43 @@ __global__ void __launch_bounds__(MmaCfg<DP, MT, F32>::NT, 1) attn_mma_kernel(co
                 const bool ok = page >= 0;
                 const int64_t ph = (int64_t)(ok ? page : 0) * H + cur.h;
                 const int64_t base = ((ph << page_log2) + (n0 & (a.c.page - 1))) * D;
-                const uint32_t dst = ring + (uint32_t)(i % STAGES) * C::UNIT + lane * 16;
+                const uint32_t st = ring + (uint32_t)(i % STAGES) * C::UNIT;
+                const uint32_t dst = st + lane * 16, vdst = st + 2 * KJ * 512 + v_slot;
+                if (ok && n0 + 16 <= end && D == DP) {
+                    const uint8_t *const ksrc = a.c.k + base + k_off, *const vsrc = a.c.v + base + v_off;
 #pragma unroll
-                for (int r = 0; r < 2; ++r)
+                    for (int r = 0; r < 2; ++r)
 #pragma unroll
-                    for (int j = 0; j < KJ; ++j) {
-                        const int row = g + 8 * r, ch = 64 * j + 16 * t;
-                        const bool on = ok && n0 + row < end && ch < D;
-                        cp16(dst + (r * KJ + j) * 512, a.c.k + (on ? base + row * D + ch : 0), on);
+                        for (int j = 0; j < KJ; ++j) cp16(dst + (r * KJ + j) * 512, ksrc + 8 * r * DP + 64 * j, true);
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        const uint8_t *src = vsrc + ((r & 1) + 8 * (r >> 1)) * DP;
+                        if (DP == 128)
+                            cp16(vdst + r * 32 * C::VB, src, true);
+                        else
+                            cp8(vdst + r * 32 * C::VB, src, true);
                     }
-                const uint32_t vdst = ring + (uint32_t)(i % STAGES) * C::UNIT + 2 * KJ * 512 + lane * C::VB;
+                } else {
 #pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const int row = 2 * t + (r & 1) + 8 * (r >> 1), ch = C::VB * g;
-                    const bool on = ok && n0 + row < end && ch < D;
-                    const uint8_t *src = a.c.v + (on ? base + row * D + ch : 0);
-                    if (DP == 128)
-                        cp16(vdst + r * 32 * C::VB, src, on);
-                    else
-                        cp8(vdst + r * 32 * C::VB, src, on);
+                    for (int r = 0; r < 2; ++r)
+#pragma unroll
+                        for (int j = 0; j < KJ; ++j) {
+                            const int row = g + 8 * r, ch = 64 * j + 16 * t;
+                            const bool on = ok && n0 + row < end && ch < D;
+                            cp16(dst + (r * KJ + j) * 512, a.c.k + (on ? base + row * D + ch : 0), on);
+                        }
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        const int row = 2 * t + (r & 1) + 8 * (r >> 1), ch = C::VB * g;
+                        const bool on = ok && n0 + row < end && ch < D;
+                        const uint8_t *src = a.c.v + (on ? base + row * D + ch : 0);
+                        if (DP == 128)
+                            cp16(vdst + r * 32 * C::VB, src, on);
+                        else
+                            cp8(vdst + r * 32 * C::VB, src, on);
+                    }
                 }
-                const uint32_t sdst = ring + (uint32_t)(i % STAGES) * C::UNIT + C::UNIT - 256 + lane * 8;
+                const uint32_t sdst = st + C::UNIT - 256 + lane * 8;
                 cp4(sdst, a.c.ks + ph, ok);
                 cp4(sdst + 4, a.c.vs + ph, ok);
             }
@@ -184,36 +206,37 @@ __global__ void __launch_bounds__(MmaCfg<DP, MT, F32>::NT, 1) attn_mma_kernel(co
         for (int i = 0; i < STAGES - 1; ++i) issue(i);
 
         // ---- Q: scaled rows as fragments in shared memory ----------------------------
-        // warp w takes rows w, w + NW, ...
-        for (int r = w; r < ROWS; r += NW) {
-            const RowPlace p = row_place(a, cur.s, cur.b, cur.rt, cur.h, r);
-            float x[DP / 32];
-            uint32_t top = 0;
+        // a warp takes 32 / LR rows at a time, LR lanes with 8 channels each a row
+        {
+            constexpr int LR = DP / 8, RW = 32 / LR;
+            const int rl = lane / LR, ch = 8 * (lane % LR);
+            for (int r0 = w * RW; r0 < ROWS; r0 += NW * RW) {
+                const int r = r0 + rl;
+                const RowPlace p = row_place(a, cur.s, cur.b, cur.rt, cur.h, r);
+                float x[8];
 #pragma unroll
-            for (int i = 0; i < DP / 32; ++i) {
-                const int d = 4 * lane + i;                  // DP = 128: 4 a lane; DP = 64: 2 a lane
-                const int ch = DP == 128 ? d : 2 * lane + i;
-                x[i] = p.valid && ch < D ? load_q(a, !F32, p.q + ch) : 0.f;
-                top = max(top, __float_as_uint(x[i]) & 0x7fffffffu);
-            }
-            top = __reduce_max_sync(0xffffffffu, top);
-            int e = (int)(top >> 23) - 127;
-            e = imax(e, -100);
-            const float inv = __int_as_float((14 - e + 127) << 23);      // e <= 127: a normal number
-            if (lane == 0)
-                factor[r] = top >= 0x7f800000u ? NAN : __int_as_float((e - 14 + 127) << 23) * a.sl2;
-            // channel d of row r: k-step (j, s), lane t', half: see the layouts above
+                for (int i = 0; i < 8; ++i) x[i] = 0.f;
+                if (p.valid && ch < D) load_q8(a, !F32, p.q + ch, x);
+                uint32_t top = 0;
 #pragma unroll
-            for (int i = 0; i < DP / 32; i += 2) {
-                const int ch = DP == 128 ? 4 * lane + i : 2 * lane + i;
-                const int j = ch >> 6, tt = (ch >> 4) & 3, s = (ch >> 2) & 3, hi = (ch >> 1) & 1;
-                const int reg = hi * 2 + ((r & 15) >> 3), ln = (r & 7) * 4 + tt;
-                const float y0 = x[i] * inv, y1 = x[i + 1] * inv;
-                const uint32_t q0 = pack_f16(y0, y1);
-                uint32_t *f = reinterpret_cast<uint32_t *>(smem + C::Q_OFF) +
-                              (((r >> 4) * C::PARTS) * KS + j * 4 + s) * 128 + ln * 4 + reg;
-                f[0] = q0;
-                if (F32) f[KS * 128] = pack_rest(y0, y1, q0);
+                for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(x[i]) & 0x7fffffffu);
+#pragma unroll
+                for (int y = LR / 2; y; y >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, y));
+                const int e = imax((int)(top >> 23) - 127, -100);
+                const float inv = __int_as_float((14 - e + 127) << 23);      // e <= 127: a normal number
+                if (ch == 0) factor[r] = top >= 0x7f800000u ? NAN : __int_as_float((e - 14 + 127) << 23) * a.sl2;
+                // channels ch .. ch + 7 of row r: two k-steps' shares of lane t'; see the layouts above
+                const int j = ch >> 6, tt = (ch >> 4) & 3, ln = (r & 7) * 4 + tt;
+#pragma unroll
+                for (int i = 0; i < 8; i += 2) {
+                    const int s = ((ch >> 2) & 3) + (i >> 2), reg = ((i >> 1) & 1) * 2 + ((r & 15) >> 3);
+                    const float y0 = x[i] * inv, y1 = x[i + 1] * inv;
+                    const uint32_t q0 = pack_f16(y0, y1);
+                    uint32_t *f = reinterpret_cast<uint32_t *>(smem + C::Q_OFF) +
+                                  (((r >> 4) * C::PARTS) * KS + j * 4 + s) * 128 + ln * 4 + reg;
+                    f[0] = q0;
+                    if (F32) f[KS * 128] = pack_rest(y0, y1, q0);
+                }
             }
         }
         __syncthreads();
@@ -232,14 +255,17 @@ __global__ void __launch_bounds__(MmaCfg<DP, MT, F32>::NT, 1) attn_mma_kernel(co
                 min_lim = imin(min_lim, lim[x][y]);
             }
         min_lim = imin(__reduce_min_sync(0xffffffffu, min_lim), end);
-        uint32_t qf[F32 || MT > 1 ? 1 : KS][4];
-        if (!F32 && MT == 1) {
+        // one row tile of bf16: Q stays in registers (from shared memory it would be half of
+        // the traffic there)
+        constexpr bool QREG = !F32 && MT == 1;
+        uint32_t qf[QREG ? KS : 1][4];
+        if (QREG)
 #pragma unroll
             for (int k = 0; k < KS; ++k) {
                 const uint4 v = lds16(sbase + C::Q_OFF + k * 512 + lane * 16);
-                qf[k][0] = v.x; qf[k][1] = v.y; qf[k][2] = v.z; qf[k][3] = v.w;
+                qf[k % (QREG ? KS : 1)][0] = v.x; qf[k % (QREG ? KS : 1)][1] = v.y;
+                qf[k % (QREG ? KS : 1)][2] = v.z; qf[k % (QREG ? KS : 1)][3] = v.w;
             }
-        }
         float o[MT][NO][4];
 #pragma unroll
         for (int x = 0; x < MT; ++x)
@@ -273,12 +299,11 @@ __global__ void __launch_bounds__(MmaCfg<DP, MT, F32>::NT, 1) attn_mma_kernel(co
 #pragma unroll
                         for (int part = C::PARTS - 1; part >= 0; --part) {
                             uint32_t f[4];
-                            if (!F32 && MT == 1) {
+                            if (QREG) {
 #pragma unroll
-                                for (int y = 0; y < 4; ++y) f[y] = qf[(j * 4 + q) % (F32 || MT > 1 ? 1 : KS)][y];
+                                for (int y = 0; y < 4; ++y) f[y] = qf[(j * 4 + q) % (QREG ? KS : 1)][y];
                             } else {
-                                const uint4 v = lds16(sbase + C::Q_OFF + ((x * C::PARTS + part) * KS + j * 4 + q) * 512 +
-                                                      lane * 16);
+                                const uint4 v = lds16(sbase + C::Q_OFF + ((x * C::PARTS + part) * KS + j * 4 + q) * 512 + lane * 16);
                                 f[0] = v.x; f[1] = v.y; f[2] = v.z; f[3] = v.w;
                             }
                             mma16816(s[x][0], f, a0, a1);
@@ -344,15 +369,21 @@ __global__ void __launch_bounds__(MmaCfg<DP, MT, F32>::NT, 1) attn_mma_kernel(co
                     }
                 }
             // O += P V
+            uint32_t vr[4][C::VB / 4];
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+                const uint32_t at = st + 2 * KJ * 512 + y * 32 * C::VB + v_slot;
+                if (DP == 128) {
+                    const uint4 v = lds16(at);
+                    vr[y][0] = v.x; vr[y][1] = v.y; vr[y][C::VB / 4 - 2] = v.z; vr[y][C::VB / 4 - 1] = v.w;
+                } else {
+                    const uint2 v = lds8(at);
+                    vr[y][0] = v.x; vr[y][1] = v.y;
+                }
+            }
 #pragma unroll
             for (int q = 0; q < C::VB / 4; ++q) {
-                uint32_t r[4];
-#pragma unroll
-                for (int y = 0; y < 4; ++y)
-                    asm volatile("ld.shared.b32 %0, [%1];"
-                                 : "=r"(r[y])
-                                 : "r"(st + 2 * KJ * 512 + y * 32 * C::VB + lane * C::VB + 4 * q)
-                                 : "memory");
+                const uint32_t r[4] = {vr[0][q], vr[1][q], vr[2][q], vr[3][q]};
                 const uint32_t lo01 = __byte_perm(r[0], r[1], 0x5140), hi01 = __byte_perm(r[0], r[1], 0x7362);
                 const uint32_t lo23 = __byte_perm(r[2], r[3], 0x5140), hi23 = __byte_perm(r[2], r[3], 0x7362);
                 const uint32_t b0[4] = {f16x2_of_e4m3x2(lo01), f16x2_of_e4m3x2_hi(lo01), f16x2_of_e4m3x2(hi01),
@@ -386,23 +417,25 @@ __global__ void __launch_bounds__(MmaCfg<DP, MT, F32>::NT, 1) attn_mma_kernel(co
                 }
             }
         __syncthreads();                             // every warp is done with its ring
+        const int rows = imin(ROWS, cur.s.n * a.G - cur.rt * ROWS);       // of this tile that are someone's
         if (w < active) {
 #pragma unroll
             for (int x = 0; x < MT; ++x)
 #pragma unroll
-                for (int j = 0; j < NO; ++j)
+                for (int y = 0; y < 2; ++y)
+                    if (16 * x + 8 * y + g < rows)
 #pragma unroll
-                    for (int y = 0; y < 2; ++y)
+                    for (int j = 0; j < NO; ++j)
                         *reinterpret_cast<float2 *>(&join[(w * ROWS + 16 * x + 8 * y + g) * C::OS + 8 * j + 2 * t]) =
                             make_float2(o[x][j][2 * y], o[x][j][2 * y + 1]);
         }
         __syncthreads();
         const bool final = k0 == 0 && k1 == cur.nt;
         const int64_t slot = (int64_t)cta * 2 + (k0 == 0 ? 1 : 0);
-        for (int i = tid; i < ROWS * (DP / 4); i += NT) {
+        for (int i = tid; i < rows * (DP / 4); i += NT) {
             const int r = i / (DP / 4), d = (i % (DP / 4)) * 4;
+            if (d >= D) continue;
             const RowPlace p = row_place(a, cur.s, cur.b, cur.rt, cur.h, r);
-            if (!p.valid || d >= D) continue;
             float M = kNoMax;
             for (int x = 0; x < active; ++x) M = fmaxf(M, m_sh[x * ROWS + r]);
             float ls = 0.f;

@@ -183,6 +183,33 @@ __device__ __forceinline__ float load_q(const AttnArgs &a, bool bf16, int64_t at
                 : reinterpret_cast<const float *>(a.Q)[at];
 }
 
+// 8 channels of a query row.
+__device__ __forceinline__ void load_q8(const AttnArgs &a, bool bf16, int64_t at, float (&x)[8]) {
+    if (bf16) {
+        const __nv_bfloat16 *q = reinterpret_cast<const __nv_bfloat16 *>(a.Q) + at;
+        if ((reinterpret_cast<uintptr_t>(q) & 15) == 0) {
+            const uint4 v = *reinterpret_cast<const uint4 *>(q);
+            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                x[2 * i] = __uint_as_float(w[i] << 16);
+                x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+            }
+            return;
+        }
+    } else {
+        const float *q = reinterpret_cast<const float *>(a.Q) + at;
+        if ((reinterpret_cast<uintptr_t>(q) & 15) == 0) {
+            const float4 u = reinterpret_cast<const float4 *>(q)[0], v = reinterpret_cast<const float4 *>(q)[1];
+            x[0] = u.x; x[1] = u.y; x[2] = u.z; x[3] = u.w;
+            x[4] = v.x; x[5] = v.y; x[6] = v.z; x[7] = v.w;
+            return;
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = load_q(a, bf16, at + i);
+}
+
 // 4 output channels d .. d+3 of a row.
 __device__ __forceinline__ void store_o4(const AttnArgs &a, bool f32, int64_t at, float4 v) {
     if (f32) {
