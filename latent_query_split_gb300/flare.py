@@ -11,7 +11,9 @@ compiled library (or without a GPU) these calls fail.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
+import struct
 from typing import NamedTuple, Optional, Sequence
 
 import torch
@@ -105,7 +107,8 @@ def load_library(build_if_missing: bool = True):
     lib.flare_pp_bwd.argtypes = [D, P, P, P, P, P, P, P, I, P, P, P, P, P, P, P, P, P, P, P, P, Z, P]
     lib.flare_encoder_fwd_noalloc.argtypes = [D, P, P, P, P, P, I, P, P, P, P, P]
     lib.flare_check_bounded_wait.argtypes = [ctypes.c_uint, P]
-    C, CP, L64 = ctypes.POINTER(FlareCacheDims), ctypes.POINTER(FlareCachePtrs), ctypes.c_int64
+    # (the token cache's two structs are passed packed, as bytes: see _cache_args)
+    C, CP, L64 = ctypes.c_char_p, ctypes.c_char_p, ctypes.c_int64
     lib.flare_cache_append.argtypes = [C, CP, P, P, L64, L64, L64, P, P, P, L64, P, P, I, I, P, P]
     lib.flare_cache_workspace_bytes.argtypes = [C, L64]
     lib.flare_cache_workspace_bytes.restype = Z
@@ -434,40 +437,74 @@ def flare_cache_alloc(num_pages: int, H: int, D: int, page: int = 64, *, page_ta
 _TOKEN_DTYPES = {torch.float32: FLARE_F32, torch.bfloat16: FLARE_BF16}
 
 
-def _cache_ptrs(cache: FlareCache):
+# The fields of FlareCacheDims and FlareCachePtrs. Packing a struct takes a third of
+# the time of filling a ctypes.Structure, which counts where a call is one token.
+_PACK_DIMS, _PACK_PTRS = struct.Struct("@6iqf2i4x").pack, struct.Struct("@5P").pack
+_raw_stream = torch._C._cuda_getCurrentRawStream
+_F8, _F32, _I32 = torch.float8_e4m3fn, torch.float32, torch.int32
+
+
+def _cache_args(cache: FlareCache):
+    """(packed pointers, device, (B, W), (P, H, page, D)) of a cache after checks."""
     k, v, ks, vs, table = cache
-    if k.dtype != torch.float8_e4m3fn or v.dtype != torch.float8_e4m3fn:
+    shape, scales, dev = k.shape, ks.shape, k.device
+    if k.dtype != _F8 or v.dtype != _F8:
         raise TypeError("a cache's codes are float8_e4m3fn")
-    if ks.dtype != torch.float32 or vs.dtype != torch.float32 or table.dtype != torch.int32:
+    if ks.dtype != _F32 or vs.dtype != _F32 or table.dtype != _I32:
         raise TypeError("a cache's scales are float32 and its page table is int32")
-    if k.dim() != 4 or table.dim() != 2 or v.shape != k.shape or ks.shape != k.shape[:2] or vs.shape != ks.shape:
+    if len(shape) != 4 or table.dim() != 2 or v.shape != shape or scales != shape[:2] or vs.shape != scales:
         raise ValueError("cache shapes do not match: k, v [P, H, page, D], scales [P, H], page_table [B, W]")
-    dev = k.device
+    if dev.type != "cuda":
+        raise ValueError("device tensor expected")
     if v.device != dev or ks.device != dev or vs.device != dev or table.device != dev:
         raise ValueError("the cache's tensors are on different devices")
-    return FlareCachePtrs(_ptr(k), _ptr(v), _ptr(ks), _ptr(vs), _ptr(table))
-
-
-def _cache_dims(cache: FlareCache, Hq: int, dtype, scale=None, kernel="auto"):
-    P, H, page, D = cache.k.shape
-    if dtype not in _TOKEN_DTYPES:
-        raise TypeError(f"unsupported token dtype {dtype}")
-    if cache.k.device.index != torch.cuda.current_device():
+    if dev.index != torch.cuda.current_device():
         raise ValueError("the cache is not on the current device")
-    B, W = cache.page_table.shape
-    return FlareCacheDims(B, H, Hq, D, page, W, P, 0.0 if scale is None else float(scale),
-                          _TOKEN_DTYPES[dtype], KERNELS[kernel])
+    if not (k.is_contiguous() and v.is_contiguous() and ks.is_contiguous() and vs.is_contiguous() and
+            table.is_contiguous()):
+        raise ValueError("contiguous tensor expected")
+    return (_PACK_PTRS(k.data_ptr(), v.data_ptr(), ks.data_ptr(), vs.data_ptr(), table.data_ptr()), dev,
+            table.shape, shape)
+
+
+def _cache_dims(rows, shape, Hq: int, dtype, scale=None, kernel="auto"):
+    """Packed sizes: rows = (B, W) of the page table, shape = (P, H, page, D)."""
+    dt = _TOKEN_DTYPES.get(dtype)
+    if dt is None:
+        raise TypeError(f"unsupported token dtype {dtype}")
+    return _PACK_DIMS(rows[0], shape[1], Hq, shape[3], shape[2], rows[1], shape[0],
+                      0.0 if scale is None else float(scale), dt, KERNELS[kernel])
+
+
+def flare_cache_dims(cache: FlareCache, Hq: int, dtype, scale: Optional[float] = None, kernel: str = "auto"):
+    """Sizes of a cache's calls (see flare_cache_workspace_bytes) for Hq query heads and
+    the tokens' and queries' type, packed as the C ABI's flare_cache_dims_t."""
+    return _cache_dims(cache.page_table.shape, cache.k.shape, Hq, dtype, scale, kernel)
 
 
 def _like(t, what, dtype, shape, device):
     """Pointer of an optional tensor after checks of its type, shape and device."""
     if t is None:
         return None
-    if t.dtype != dtype or tuple(t.shape) != tuple(shape):
+    if t.dtype != dtype or t.shape != shape:
         raise ValueError(f"{what} must be {dtype} of shape {tuple(shape)}")
     if t.device != device:
         raise ValueError(f"{what} is on another device than the cache")
-    return _ptr(t)
+    if not t.is_contiguous():
+        raise ValueError(f"{what} must be contiguous")
+    return t.data_ptr()
+
+
+def _on_stream(call):
+    """A cache call with `stream` given runs with that stream current: what it
+    allocates is then ordered with its kernels, not with another stream's."""
+    @functools.wraps(call)
+    def on(*args, stream=None, **kw):
+        if stream is None:
+            return call(*args, **kw)
+        with torch.cuda.stream(stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream))):
+            return call(*args, **kw)
+    return on
 
 
 def _rows(x, what, heads, D, B, cu, dtype, device):
@@ -476,11 +513,12 @@ def _rows(x, what, heads, D, B, cu, dtype, device):
     evenly spaced."""
     if x.dtype != dtype:
         raise TypeError(f"{what} must be {dtype}")
-    if x.dim() != (4 if cu is None else 3) or x.shape[-2:] != (heads, D) or (cu is None and x.shape[0] != B):
+    shape = x.shape
+    if len(shape) != (4 if cu is None else 3) or shape[-2] != heads or shape[-1] != D or (cu is None and shape[0] != B):
         raise ValueError(f"{what} must be [B, n, {heads}, {D}], or [T, {heads}, {D}] with cu_seqlens")
     if x.device != device:
         raise ValueError(f"{what} is on another device than the cache")
-    T = x.shape[0] * x.shape[1] if cu is None else x.shape[0]
+    T = shape[0] * shape[1] if cu is None else shape[0]
     if x.is_contiguous():
         return x.data_ptr(), 0, T
     st = x.stride()
@@ -493,141 +531,162 @@ def _rows(x, what, heads, D, B, cu, dtype, device):
     return x.data_ptr(), (step if T > 1 else 0), T
 
 
+@_on_stream
 def flare_cache_append(cache: FlareCache, K, V, seq_lens, *, cu_seqlens=None, Q=None, inv_freq=None,
-                       interleaved=False, Q_out=None, seq_lens_out=None, stream=None):
+                       interleaved=False, Q_out=None, seq_lens_out=None):
     """New tokens K, V ([B,n,H,D], or [T,H,D] with int32 cu_seqlens [B+1]) enter
     the cache behind the seq_lens tokens that each sequence holds; with inv_freq
     (fp32 [rot/2]) keys and the queries Q are rotated by their positions.
     Returns (seq_lens_out, Q_out)."""
-    lib = load_library()
-    ptrs = _cache_ptrs(cache)
-    dev = cache.k.device
-    B, H, D = cache.page_table.shape[0], cache.k.shape[1], cache.k.shape[3]
-    dims = _cache_dims(cache, 0 if Q is None else Q.shape[-2], K.dtype)
-    k, k_st, T = _rows(K, "K", H, D, B, cu_seqlens, K.dtype, dev)
-    v, v_st, Tv = _rows(V, "V", H, D, B, cu_seqlens, K.dtype, dev)
-    q, q_st, Tq = (None, 0, T) if Q is None else _rows(Q, "Q", dims.Hq, D, B, cu_seqlens, K.dtype, dev)
-    if Tv != T or Tq != T:
+    lib = _lib or load_library()
+    ptrs, dev, table, shape = _cache_args(cache)
+    (B, _), (_, H, _, D), dtype = table, shape, K.dtype
+    Hq = 0 if Q is None else Q.shape[-2]
+    dims = _cache_dims(table, shape, Hq, dtype)
+    k, k_st, T = _rows(K, "K", H, D, B, cu_seqlens, dtype, dev)
+    v, v_st, Tv = _rows(V, "V", H, D, B, cu_seqlens, dtype, dev)
+    q, q_st, q_out = None, 0, None
+    if Q is not None:
+        q, q_st, Tq = _rows(Q, "Q", Hq, D, B, cu_seqlens, dtype, dev)
+        if Q_out is None:
+            Q_out = torch.empty_like(Q, memory_format=torch.contiguous_format)
+            q_out = Q_out.data_ptr()
+        else:
+            q_out = _like(Q_out, "Q_out", dtype, Q.shape, dev)
+        if Tq != T:
+            raise ValueError("K, V and Q have different numbers of tokens")
+    if Tv != T:
         raise ValueError("K, V and Q have different numbers of tokens")
-    if Q is not None and Q_out is None:
-        Q_out = torch.empty(Q.shape, dtype=Q.dtype, device=dev)
+    lens = _like(seq_lens, "seq_lens", _I32, (B,), dev)
     if seq_lens_out is None:
         seq_lens_out = torch.empty_like(seq_lens)
-    if inv_freq is not None and (inv_freq.dim() != 1 or inv_freq.shape[0] < 1):
-        raise ValueError("inv_freq must be [rot / 2]")
-    rot = 0 if inv_freq is None else 2 * inv_freq.shape[0]
-    _check(lib.flare_cache_append(
-        ctypes.byref(dims), ctypes.byref(ptrs), k, v, k_st, v_st, T,
-        _like(seq_lens, "seq_lens", torch.int32, (B,), dev),
-        _like(cu_seqlens, "cu_seqlens", torch.int32, (B + 1,), dev), q, q_st,
-        None if Q is None else _like(Q_out, "Q_out", K.dtype, Q.shape, dev),
-        _like(inv_freq, "inv_freq", torch.float32, (rot // 2,), dev), rot, int(interleaved),
-        _like(seq_lens_out, "seq_lens_out", torch.int32, (B,), dev), _stream(stream)))
+    rot = 0
+    if inv_freq is not None:
+        if inv_freq.dim() != 1 or inv_freq.shape[0] < 1:
+            raise ValueError("inv_freq must be [rot / 2]")
+        rot = 2 * inv_freq.shape[0]
+    status = lib.flare_cache_append(
+        dims, ptrs, k, v, k_st, v_st, T, lens, _like(cu_seqlens, "cu_seqlens", _I32, (B + 1,), dev), q, q_st, q_out,
+        _like(inv_freq, "inv_freq", _F32, (rot // 2,), dev), rot, int(interleaved),
+        _like(seq_lens_out, "seq_lens_out", _I32, (B,), dev), _raw_stream(dev.index))
+    if status:
+        _check(status)
     return seq_lens_out, Q_out
 
 
-def flare_cache_workspace_bytes(dims: FlareCacheDims, T: int) -> int:
-    n = load_library().flare_cache_workspace_bytes(ctypes.byref(dims), T)
-    if n == ctypes.c_size_t(-1).value:
+def flare_cache_workspace_bytes(dims, T: int) -> int:
+    """Workspace bytes of T query rows for sizes `dims` (flare_cache_dims)."""
+    n = (_lib or load_library()).flare_cache_workspace_bytes(dims, T)
+    if n == _BAD_SIZE:
         _check(FLARE_ERR_INVALID_ARG)
-    return int(n)
+    return n
+
+
+_BAD_SIZE = ctypes.c_size_t(-1).value
 
 
 def _cache_workspace(dims, T, workspace, device):
     if workspace is None:
-        workspace = torch.empty(max(flare_cache_workspace_bytes(dims, T), 1), dtype=torch.uint8, device=device)
-    elif workspace.device != device:
+        n = flare_cache_workspace_bytes(dims, T)
+        workspace = torch.empty(n, dtype=torch.uint8, device=device)
+        return workspace, workspace.data_ptr(), n
+    if workspace.device != device:
         raise ValueError("workspace is on another device than the cache")
-    return _ptr(workspace), workspace.numel() * workspace.element_size()
+    return workspace, _ptr(workspace), workspace.numel() * workspace.element_size()
 
 
+@_on_stream
 def flare_cache_attn(Q, cache: FlareCache, seq_lens, *, cu_seqlens=None, causal=True, O=None, L=None,
-                     workspace=None, scale=None, kernel="auto", stream=None):
+                     workspace=None, scale=None, kernel="auto"):
     """Attention of Q ([B,n,Hq,D], or [T,Hq,D] with int32 cu_seqlens [B+1]) over
     the seq_lens tokens that the cache holds for each sequence; returns (O, L):
     O like Q, L fp32 without the channels."""
-    lib = load_library()
-    ptrs = _cache_ptrs(cache)
-    dev = cache.k.device
-    B, D = cache.page_table.shape[0], cache.k.shape[3]
-    dims = _cache_dims(cache, Q.shape[-2], Q.dtype, scale, kernel)
-    q, q_st, T = _rows(Q, "Q", dims.Hq, D, B, cu_seqlens, Q.dtype, dev)
+    lib = _lib or load_library()
+    ptrs, dev, table, shape = _cache_args(cache)
+    B, dtype, rows = table[0], Q.dtype, Q.shape
+    Hq = rows[-2]
+    dims = _cache_dims(table, shape, Hq, dtype, scale, kernel)
+    q, q_st, T = _rows(Q, "Q", Hq, shape[3], B, cu_seqlens, dtype, dev)
     if O is None:
-        O = torch.empty(Q.shape, dtype=Q.dtype, device=dev)
+        O = torch.empty_like(Q, memory_format=torch.contiguous_format)
+        o = O.data_ptr()
+    else:
+        o = _like(O, "O", dtype, rows, dev)
     if L is None:
-        L = torch.empty(Q.shape[:-1], dtype=torch.float32, device=dev)
-    ws, nbytes = _cache_workspace(dims, T, workspace, dev)
-    _check(lib.flare_cache_attn(
-        ctypes.byref(dims), ctypes.byref(ptrs), q, q_st, T,
-        _like(seq_lens, "seq_lens", torch.int32, (B,), dev),
-        _like(cu_seqlens, "cu_seqlens", torch.int32, (B + 1,), dev), int(causal),
-        _like(O, "O", Q.dtype, Q.shape, dev), _like(L, "L", torch.float32, Q.shape[:-1], dev), ws, nbytes,
-        _stream(stream)))
+        L = torch.empty(rows[:-1], dtype=_F32, device=dev)
+        l = L.data_ptr()
+    else:
+        l = _like(L, "L", _F32, rows[:-1], dev)
+    workspace, ws, nbytes = _cache_workspace(dims, T, workspace, dev)
+    status = lib.flare_cache_attn(
+        dims, ptrs, q, q_st, T, _like(seq_lens, "seq_lens", _I32, (B,), dev),
+        _like(cu_seqlens, "cu_seqlens", _I32, (B + 1,), dev), int(causal), o, l, ws, nbytes,
+        _raw_stream(dev.index))
+    if status:
+        _check(status)
     return O, L
 
 
-def _latents(Q, cache):
-    """(M, q_batch_stride) of latent queries [H,M,D] or [B,H,M,D]."""
-    B, H, D = cache.page_table.shape[0], cache.k.shape[1], cache.k.shape[3]
+def _latents(Q, B, shape, device):
+    """(pointer, M, q_batch_stride) of latent queries [H,M,D] or [B,H,M,D]."""
+    _, H, _, D = shape
     M = Q.shape[-2]
-    if tuple(Q.shape) not in ((H, M, D), (B, H, M, D)) or Q.device != cache.k.device:
+    if Q.shape not in ((H, M, D), (B, H, M, D)) or Q.device != device:
         raise ValueError("Q must be [H, M, D] or [B, H, M, D] on the cache's device")
-    return M, (0 if Q.dim() == 3 else H * M * D)
+    return _ptr(Q), M, (0 if Q.dim() == 3 else H * M * D)
 
 
+@_on_stream
 def flare_cache_encoder_fwd(Q, cache: FlareCache, seq_lens, *, Z=None, L=None, workspace=None, scale=None,
-                            kernel="auto", stream=None):
+                            kernel="auto"):
     """The FLARE encoder over the cached tokens: latent queries Q ([H,M,D] or
     [B,H,M,D]); returns (Z [B,H,M,D], L [B,H,M]) in fp32."""
-    lib = load_library()
-    ptrs = _cache_ptrs(cache)
-    dev = cache.k.device
-    B, H, D = cache.page_table.shape[0], cache.k.shape[1], cache.k.shape[3]
-    M, qbs = _latents(Q, cache)
-    dims = _cache_dims(cache, H, Q.dtype, scale, kernel)
-    f32 = dict(dtype=torch.float32, device=dev)
+    lib = _lib or load_library()
+    ptrs, dev, table, shape = _cache_args(cache)
+    (B, _), (_, H, _, D) = table, shape
+    q, M, qbs = _latents(Q, B, shape, dev)
+    dims = _cache_dims(table, shape, H, Q.dtype, scale, kernel)
     if Z is None:
-        Z = torch.empty((B, H, M, D), **f32)
+        Z = torch.empty((B, H, M, D), dtype=_F32, device=dev)
     if L is None:
-        L = torch.empty((B, H, M), **f32)
-    ws, nbytes = _cache_workspace(dims, B * M, workspace, dev)
+        L = torch.empty((B, H, M), dtype=_F32, device=dev)
+    workspace, ws, nbytes = _cache_workspace(dims, B * M, workspace, dev)
     _check(lib.flare_cache_encoder_fwd(
-        ctypes.byref(dims), ctypes.byref(ptrs), M, _ptr(Q), qbs,
-        _like(seq_lens, "seq_lens", torch.int32, (B,), dev), _like(Z, "Z", torch.float32, (B, H, M, D), dev),
-        _like(L, "L", torch.float32, (B, H, M), dev), ws, nbytes, _stream(stream)))
+        dims, ptrs, M, q, qbs, _like(seq_lens, "seq_lens", _I32, (B,), dev), _like(Z, "Z", _F32, (B, H, M, D), dev),
+        _like(L, "L", _F32, (B, H, M), dev), ws, nbytes, _raw_stream(dev.index)))
     return Z, L
 
 
+@_on_stream
 def flare_cache_fwd(Q, cache: FlareCache, K, V, seq_lens, *, seq_lens_out=None, Y=None, Z=None, L=None,
-                    workspace=None, scale=None, kernel="auto", stream=None):
+                    workspace=None, scale=None, kernel="auto"):
     """FLARE mixer forward over a growing token set: K, V [B,N,H,D] enter the
     cache, the latents Q gather Z from all the tokens held, the new tokens decode
     against them; returns (Y [B,N,H,D], Z, L, seq_lens_out)."""
-    lib = load_library()
-    ptrs = _cache_ptrs(cache)
-    dev = cache.k.device
-    B, H, D = cache.page_table.shape[0], cache.k.shape[1], cache.k.shape[3]
-    M, qbs = _latents(Q, cache)
-    dims = _cache_dims(cache, H, Q.dtype, scale, kernel)
+    lib = _lib or load_library()
+    ptrs, dev, table, shape = _cache_args(cache)
+    (B, _), (_, H, _, D) = table, shape
+    q, M, qbs = _latents(Q, B, shape, dev)
+    dims = _cache_dims(table, shape, H, Q.dtype, scale, kernel)
     if K.dim() != 4:
         raise ValueError("K must be [B, N, H, D]")
     N = K.shape[1]
-    shape, f32 = (B, N, H, D), dict(dtype=torch.float32, device=dev)
+    tokens = (B, N, H, D)
     if Y is None:
-        Y = torch.empty(shape, dtype=Q.dtype, device=dev)
+        Y = torch.empty(tokens, dtype=Q.dtype, device=dev)
     if Z is None:
-        Z = torch.empty((B, H, M, D), **f32)
+        Z = torch.empty((B, H, M, D), dtype=_F32, device=dev)
     if L is None:
-        L = torch.empty((B, H, M), **f32)
+        L = torch.empty((B, H, M), dtype=_F32, device=dev)
+    lens = _like(seq_lens, "seq_lens", _I32, (B,), dev)
     if seq_lens_out is None:
         seq_lens_out = torch.empty_like(seq_lens)
-    ws, nbytes = _cache_workspace(dims, B * M, workspace, dev)
+    workspace, ws, nbytes = _cache_workspace(dims, B * M, workspace, dev)
     _check(lib.flare_cache_fwd(
-        ctypes.byref(dims), ctypes.byref(ptrs), M, N, _ptr(Q), qbs, _like(K, "K", Q.dtype, shape, dev),
-        _like(V, "V", Q.dtype, shape, dev), _like(seq_lens, "seq_lens", torch.int32, (B,), dev),
-        _like(seq_lens_out, "seq_lens_out", torch.int32, (B,), dev), _like(Y, "Y", Q.dtype, shape, dev),
-        _like(Z, "Z", torch.float32, (B, H, M, D), dev), _like(L, "L", torch.float32, (B, H, M), dev), ws,
-        nbytes, _stream(stream)))
+        dims, ptrs, M, N, q, qbs, _like(K, "K", Q.dtype, tokens, dev), _like(V, "V", Q.dtype, tokens, dev), lens,
+        _like(seq_lens_out, "seq_lens_out", _I32, (B,), dev), _like(Y, "Y", Q.dtype, tokens, dev),
+        _like(Z, "Z", _F32, (B, H, M, D), dev), _like(L, "L", _F32, (B, H, M), dev), ws, nbytes,
+        _raw_stream(dev.index)))
     return Y, Z, L, seq_lens_out
 
 

@@ -35,6 +35,9 @@ def _cache(**kw):
 def test_dims_struct_layout_matches_header():
     assert ctypes.sizeof(flare.FlareCacheDims) == 48 and flare.FlareCacheDims.P.offset == 24
     assert ctypes.sizeof(flare.FlareCachePtrs) == 40
+    d = _dims(B=1, H=2, Hq=4, D=64, page=16, W=7, P=2 ** 33, scale=0.5, dtype=1, kernel=2)
+    assert flare._PACK_DIMS(1, 2, 4, 64, 16, 7, 2 ** 33, 0.5, 1, 2) == bytes(d)
+    assert flare._PACK_PTRS(*A[:5]) == bytes(_cache())
 
 
 BAD_DIMS = [(dict(B=-1), INVALID), (dict(H=0), INVALID), (dict(Hq=3), INVALID), (dict(Hq=-2), INVALID),
@@ -47,12 +50,12 @@ BAD_DIMS = [(dict(B=-1), INVALID), (dict(H=0), INVALID), (dict(Hq=3), INVALID), 
 
 def _append(lib, dims, cache=None, K=A[5], V=A[6], ks=0, vs=0, T=4, lens=A[7], cu=None, Q=A[8], qs=0, Qo=A[9],
             f=A[10], rot=64, out=A[11]):
-    return lib.flare_cache_append(ctypes.byref(dims), ctypes.byref(cache or _cache()), K, V, ks, vs, T, lens, cu, Q, qs,
+    return lib.flare_cache_append(bytes(dims), bytes(cache or _cache()), K, V, ks, vs, T, lens, cu, Q, qs,
                                   Qo, f, rot, 0, out, None)
 
 
 def _attn(lib, dims, cache=None, Q=A[8], qs=0, T=4, lens=A[7], cu=None, O=A[9], L=A[10], ws=1 << 40, wsb=1 << 40):
-    return lib.flare_cache_attn(ctypes.byref(dims), ctypes.byref(cache or _cache()), Q, qs, T, lens, cu, 1, O, L, ws, wsb,
+    return lib.flare_cache_attn(bytes(dims), bytes(cache or _cache()), Q, qs, T, lens, cu, 1, O, L, ws, wsb,
                                 None)
 
 
@@ -61,10 +64,10 @@ def test_bad_sizes_are_refused(lib, change, status):
     d = _dims(**change)
     assert _append(lib, d) == status and _attn(lib, d) == status
     assert lib.flare_last_error_string()
-    assert lib.flare_cache_workspace_bytes(ctypes.byref(d), 4) == ctypes.c_size_t(-1).value
-    assert lib.flare_cache_encoder_fwd(ctypes.byref(d), ctypes.byref(_cache()), 16, A[5], 0, A[6], A[7], A[8], A[9], 1 << 40,
+    assert lib.flare_cache_workspace_bytes(bytes(d), 4) == ctypes.c_size_t(-1).value
+    assert lib.flare_cache_encoder_fwd(bytes(d), bytes(_cache()), 16, A[5], 0, A[6], A[7], A[8], A[9], 1 << 40,
                                        None) == status
-    assert lib.flare_cache_fwd(ctypes.byref(d), ctypes.byref(_cache()), 16, 3, A[5], 0, A[6], A[7], A[8], A[9], A[10], A[11],
+    assert lib.flare_cache_fwd(bytes(d), bytes(_cache()), 16, 3, A[5], 0, A[6], A[7], A[8], A[9], A[10], A[11],
                                A[12], 1 << 40, 1 << 40, None) == status
 
 
@@ -89,7 +92,7 @@ def test_attn_refuses(lib, kw):
 
 
 def test_attn_needs_its_workspace_and_query_heads(lib):
-    need = lib.flare_cache_workspace_bytes(ctypes.byref(_dims()), 4)
+    need = lib.flare_cache_workspace_bytes(bytes(_dims()), 4)
     assert need > 0
     assert _attn(lib, _dims(), wsb=need - 1) == WORKSPACE and _attn(lib, _dims(), ws=None) == WORKSPACE
     assert _attn(lib, _dims(Hq=0)) == INVALID
@@ -99,13 +102,13 @@ def test_attn_needs_its_workspace_and_query_heads(lib):
 
 def test_nothing_to_do_is_fine(lib):
     assert _attn(lib, _dims(B=0), T=0) == 0 and _attn(lib, _dims(), T=0) == 0
-    assert lib.flare_cache_workspace_bytes(ctypes.byref(_dims()), 0) == 0
+    assert lib.flare_cache_workspace_bytes(bytes(_dims()), 0) == 0
 
 
 def test_mixer_checks_every_stage_before_launching(lib):
     def call(d=None, M=16, N=3, Q=A[5], qbs=0, K=A[6], V=A[7], lens=A[8], out=A[9], Y=A[10], Z=A[11], L=A[12],
              ws=1 << 40, wsb=1 << 40):
-        return lib.flare_cache_fwd(ctypes.byref(d or _dims()), ctypes.byref(_cache()), M, N, Q, qbs, K, V, lens, out, Y, Z, L,
+        return lib.flare_cache_fwd(bytes(d or _dims()), bytes(_cache()), M, N, Q, qbs, K, V, lens, out, Y, Z, L,
                                    ws, wsb, None)
     for kw in (dict(M=0), dict(N=-1), dict(Q=None), dict(qbs=5), dict(K=None), dict(V=None), dict(lens=None), dict(out=None),
                dict(out=A[8]), dict(Y=None), dict(Z=None), dict(L=None), dict(ws=1 + (1 << 40))):
@@ -119,13 +122,13 @@ def test_binding_refuses_what_it_cannot_pass_on():
     cache = flare.flare_cache_alloc(8, 2, 64, 16, page_table=table, device="cpu")
     assert cache.k.shape == (8, 2, 16, 64) and cache.v_scale.shape == (8, 2)
     with pytest.raises(ValueError):
-        flare._cache_ptrs(cache)                                                   # not on a device
+        flare._cache_args(cache)                                                   # not on a device
     with pytest.raises(TypeError):
-        flare._cache_ptrs(cache._replace(k=cache.k.float()))
+        flare._cache_args(cache._replace(k=cache.k.float()))
     with pytest.raises(TypeError):
-        flare._cache_ptrs(cache._replace(page_table=table.long()))
+        flare._cache_args(cache._replace(page_table=table.long()))
     with pytest.raises(ValueError):
-        flare._cache_ptrs(cache._replace(v=cache.v[:4]))
+        flare._cache_args(cache._replace(v=cache.v[:4]))
     x = torch.zeros((2, 3, 2, 64), dtype=torch.bfloat16)
     rows = lambda x, cu=None, heads=2: flare._rows(x, "K", heads, 64, 2, cu, torch.bfloat16, x.device)  # noqa: E731
     assert rows(x)[1:] == (0, 6)

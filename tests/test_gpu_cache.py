@@ -329,7 +329,7 @@ def test_attn(kernel, dtype, H, G, D, page, lens, counts, causal):
     T, Hq = Q.shape[:2]
     O, go = guarded((T + 2, Hq, D), DT[dtype], fill=7.0)
     L, gl = guarded((T + 2, Hq), fill=7.0)
-    need = flare.flare_cache_workspace_bytes(flare._cache_dims(cache, Hq, Q.dtype, kernel=kernel), T + 2)
+    need = flare.flare_cache_workspace_bytes(flare.flare_cache_dims(cache, Hq, Q.dtype, kernel=kernel), T + 2)
     ws, gw = guarded((need,), torch.uint8)
     tail = torch.full((2, Hq, D), math.nan, dtype=Q.dtype, device="cuda")       # rows behind the last sequence
     flare.flare_cache_attn(torch.cat((Q, tail)), cache, ints(lens), cu_seqlens=starts(counts), causal=causal, O=O, L=L,
@@ -532,7 +532,7 @@ def test_captured_step_follows_the_lengths(n):
     K, V = (torch.zeros((B, n, H, D), dtype=torch.bfloat16, device="cuda") for _ in range(2))
     Q = torch.zeros((B, n, H * G, D), dtype=torch.bfloat16, device="cuda")
     O, L, after = torch.empty_like(Q), torch.empty(Q.shape[:-1], device="cuda"), torch.empty_like(lens)
-    ws = torch.empty(flare.flare_cache_workspace_bytes(flare._cache_dims(cache, H * G, Q.dtype), B * n), dtype=torch.uint8,
+    ws = torch.empty(flare.flare_cache_workspace_bytes(flare.flare_cache_dims(cache, H * G, Q.dtype), B * n), dtype=torch.uint8,
                      device="cuda")
     f = freqs(D)
 
