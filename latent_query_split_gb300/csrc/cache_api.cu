@@ -88,9 +88,9 @@ Pool make_pool(const flare_cache_dims_t *d, const flare_cache_t *c) {
     return p;
 }
 
-AttnPlan plan_for(const flare_cache_dims_t *d, int G, int64_t T) {
+AttnPlan plan_for(const flare_cache_dims_t *d, int G, int64_t T, bool ragged) {
     const flare_cache_t none = {};
-    return attn_plan(make_pool(d, &none), G, d->dtype == FLARE_BF16, T, d->kernel, planning_multiprocessors());
+    return attn_plan(make_pool(d, &none), G, d->dtype == FLARE_BF16, T, ragged, d->kernel, planning_multiprocessors());
 }
 
 // Strides of one call's rows, in elements.
@@ -110,7 +110,7 @@ flare_status_t attn_run(const flare_cache_dims_t *d, const flare_cache_t *cache,
     const size_t es = elem_size(d);
     if (!aligned(Q, es) || !aligned(O, o_f32 ? 4 : es) || !aligned(L, 4))
         return fail(FLARE_ERR_INVALID_ARG, "tensors must be aligned to their element size");
-    const AttnPlan plan = plan_for(d, G, T);
+    const AttnPlan plan = plan_for(d, G, T, cu != nullptr);
     if (!ws || ws_bytes < plan.bytes)
         return fail(FLARE_ERR_WORKSPACE, "workspace of %zu bytes required, %zu given", plan.bytes, ws_bytes);
     if (!aligned(ws, 256)) return fail(FLARE_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
@@ -138,7 +138,7 @@ flare_status_t attn_run(const flare_cache_dims_t *d, const flare_cache_t *cache,
     a.rec = (int4 *)((char *)ws + plan.rec);
     int sms;
     if ((s = device_facts(&sms, &a.status)) != FLARE_OK) return s;
-    const cudaError_t e = launch_attn(a, plan.kernel, d->dtype == FLARE_BF16, st);
+    const cudaError_t e = launch_attn(a, plan, d->dtype == FLARE_BF16, st);
     return e == cudaSuccess ? FLARE_OK
                             : fail(FLARE_ERR_CUDA, "cache attention launch: %s", cudaGetErrorString(e));
 }
@@ -229,7 +229,7 @@ size_t flare_cache_workspace_bytes(const flare_cache_dims_t *dims, int64_t T) {
         fail(FLARE_ERR_INVALID_ARG, "Hq=%d, T=%lld: no query rows", dims->Hq, (long long)T);
         return (size_t)-1;
     }
-    return T == 0 || dims->B == 0 ? 0 : plan_for(dims, dims->Hq / dims->H, T).bytes;
+    return T == 0 || dims->B == 0 ? 0 : plan_for(dims, dims->Hq / dims->H, T, true).bytes;
 }
 
 flare_status_t flare_cache_attn(const flare_cache_dims_t *dims, const flare_cache_t *cache, const void *Q,

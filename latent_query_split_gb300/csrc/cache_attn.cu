@@ -18,7 +18,7 @@ namespace cache {
 // fp32 FMA on exactly converted codes. The reads are as few as they can be
 // for one head's rows; the FMAs bound it from some four rows on.
 template <int R, bool BF16>
-__global__ void __launch_bounds__(128) attn_simt_kernel(const AttnArgs a) {
+__global__ void __launch_bounds__(128) attn_simt_kernel(const __grid_constant__ AttnArgs a) {
     constexpr int NT = 128, NW = 4;
     __shared__ int64_t scan_sh[NW];
     __shared__ Cursor cur_sh;
@@ -175,7 +175,7 @@ __global__ void __launch_bounds__(128) attn_simt_kernel(const AttnArgs a) {
 // spans first .. blockIdx.x, the first in slot 1 (it began there) and the rest
 // in slot 0. They are added in that order, so results do not vary. A piece
 // without a visible token has l = 0. Bound by latency: a few KB a row.
-__global__ void __launch_bounds__(128) attn_merge_kernel(const AttnArgs a, const int f32) {
+__global__ void __launch_bounds__(128) attn_merge_kernel(const __grid_constant__ AttnArgs a, const int f32) {
     tc::pdl_wait();
     const int4 rec = a.rec[blockIdx.x];
     if (rec.x < 0) return;
@@ -223,7 +223,7 @@ __global__ void __launch_bounds__(128) attn_merge_kernel(const AttnArgs a, const
 }
 
 // ---- choice and launch ----------------------------------------------------------------
-AttnPlan attn_plan(const Pool &c, int G, bool bf16, int64_t T, int family, int sms) {
+AttnPlan attn_plan(const Pool &c, int G, bool bf16, int64_t T, bool ragged, int family, int sms) {
     AttnPlan p;
     p.kernel = family == FLARE_KERNEL_SIMT ? AttnKernel::kSimt : AttnKernel::kMma;
     const int64_t per_seq = c.B > 0 ? T * G / c.B : 0;      // rows of a head and sequence on average
@@ -232,6 +232,15 @@ AttnPlan attn_plan(const Pool &c, int G, bool bf16, int64_t T, int family, int s
              : bf16 && per_seq > 16        ? 32
                                            : 16;
     int64_t grid = (int64_t)sms * (p.kernel == AttnKernel::kSimt ? 4 : p.kernel == AttnKernel::kMma ? 2 : 1);
+    // Few items of few tokens: clusters of blocks and no merge. Two blocks fit a
+    // multiprocessor; a block's share stays under 4096 tokens, beyond which equal spans over
+    // all multiprocessors gain more than the second launch costs.
+    p.cluster = 1;
+    if (p.kernel == AttnKernel::kMma && !ragged && c.B > 0) {
+        const int64_t items = (T / c.B * G + p.rows - 1) / p.rows * c.B * c.H;
+        for (int s = 8; s > 1 && p.cluster == 1; s /= 2)
+            if (items * s <= 2 * sms && (int64_t)c.W * c.page <= 4096 * s) p.cluster = s;
+    }
     // no more spans than there can be tiles
     const int64_t tiles = ((T * G + p.rows - 1) / p.rows + c.B) * c.H *
                           (((int64_t)c.W * c.page + kTile - 1) / kTile + 1);
@@ -263,7 +272,8 @@ cudaError_t launch_pdl(Kernel k, dim3 grid, dim3 block, cudaStream_t st, Args...
 }
 }  // namespace
 
-cudaError_t launch_attn(const AttnArgs &a, AttnKernel kernel, bool bf16, cudaStream_t st) {
+cudaError_t launch_attn(const AttnArgs &a, const AttnPlan &plan, bool bf16, cudaStream_t st) {
+    const AttnKernel kernel = plan.kernel;
     cudaError_t e;
     if (kernel == AttnKernel::kSimt) {
         if (bf16)
@@ -275,9 +285,9 @@ cudaError_t launch_attn(const AttnArgs &a, AttnKernel kernel, bool bf16, cudaStr
     } else if (kernel == AttnKernel::kTc) {
         e = launch_attn_tc(a, st);
     } else {
-        e = launch_attn_mma(a, bf16, st);
+        e = launch_attn_mma(a, bf16, plan.cluster, st);
     }
-    if (e != cudaSuccess) return e;
+    if (e != cudaSuccess || plan.cluster > 1) return e;
     e = launch_pdl(attn_merge_kernel, dim3(a.grid, (a.rows + 3) / 4), dim3(128), st, a,
                    (int)(!bf16 || a.o_f32));
     if (e != cudaSuccess) return e;

@@ -84,7 +84,39 @@ __device__ __forceinline__ uint32_t pack_rest(float lo, float hi, uint32_t kept)
     return pack_f16(lo - k.x, hi - k.y);
 }
 
-template <int DP, int MT, bool F32>
+__device__ __forceinline__ int cluster_rank() {
+    int r;
+    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ int cluster_size() {
+    int r;
+    asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// Shared memory of block `rank` of the cluster at this block's address `at`.
+__device__ __forceinline__ float4 ld_peer4(uint32_t at, int rank) {
+    float4 v;
+    asm volatile("{\n\t.reg .b32 p;\n\tmapa.shared::cluster.u32 p, %4, %5;\n\t"
+                 "ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [p];\n\t}"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(at), "r"(rank)
+                 : "memory");
+    return v;
+}
+__device__ __forceinline__ float2 ld_peer2(uint32_t at, int rank) {
+    float2 v;
+    asm volatile("{\n\t.reg .b32 p;\n\tmapa.shared::cluster.u32 p, %2, %3;\n\tld.shared::cluster.v2.f32 {%0, %1}, [p];\n\t}"
+                 : "=f"(v.x), "=f"(v.y)
+                 : "r"(at), "r"(rank)
+                 : "memory");
+    return v;
+}
+
+template <int DP, int MT, bool F32, bool CL>
 struct MmaCfg {
     // two blocks a multiprocessor: one's loads run while the other joins its warps, writes and
     // begins its next piece
@@ -96,20 +128,25 @@ struct MmaCfg {
     static constexpr int PARTS = F32 ? 2 : 1;
     static constexpr int VB = DP / 8;                     // bytes of a value row a lane holds
     static constexpr uint32_t UNIT = 32 * (2 * KJ * 16 + 4 * VB) + 256;   // codes, then the scales
-    static constexpr int STAGES = DP == 128 ? (NW == 6 ? 4 : 5) : 8;
+    static constexpr int STAGES = (DP == 128 ? (NW == 6 ? 4 : 5) : 8) - (CL ? 1 : 0);
     static constexpr uint32_t RING = NW * STAGES * UNIT;
     static constexpr uint32_t OS = DP + 8;                // padded row of the joining buffer
     static constexpr uint32_t JOIN = NW * ROWS * OS * 4;
     static constexpr uint32_t Q_OFF = RING > JOIN ? RING : JOIN;
     static constexpr uint32_t Q_BYTES = MT * PARTS * KS * 512;
     static constexpr uint32_t ML_OFF = Q_OFF + Q_BYTES;   // m, l of each warp and row; row factors
-    static constexpr uint32_t BYTES = ML_OFF + 2 * NW * ROWS * 4 + ROWS * 4;
+    // a cluster's exchange: this block's O, m and l of each row
+    static constexpr uint32_t EX_OFF = (ML_OFF + 2 * NW * ROWS * 4 + ROWS * 4 + 15) / 16 * 16;
+    static constexpr uint32_t BYTES = EX_OFF + (CL ? ROWS * (DP * 4 + 8) : 0);
     static_assert(2 * (BYTES + 1024 + 512) <= 233472, "shared memory of two CTAs exceeded");
 };
 
-template <int DP, int MT, bool F32>
-__global__ void __launch_bounds__(MmaCfg<DP, MT, F32>::NT, 2) attn_mma_kernel(const AttnArgs a) {
-    using C = MmaCfg<DP, MT, F32>;
+// CL: a cluster of blocks takes one item, each block an equal share of its tokens,
+// and joins them through distributed shared memory: one launch and no workspace,
+// for calls so small that a second launch would cost as much as the attention.
+template <int DP, int MT, bool F32, bool CL>
+__global__ void __launch_bounds__(MmaCfg<DP, MT, F32, CL>::NT, 2) attn_mma_kernel(const __grid_constant__ AttnArgs a) {
+    using C = MmaCfg<DP, MT, F32, CL>;
     constexpr int NW = C::NW, NT = C::NT, ROWS = C::ROWS, KJ = C::KJ, KS = C::KS, NO = C::NO, STAGES = C::STAGES;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ int64_t scan_sh[NW];
@@ -126,16 +163,42 @@ __global__ void __launch_bounds__(MmaCfg<DP, MT, F32>::NT, 2) attn_mma_kernel(co
     float *const join = reinterpret_cast<float *>(smem);
     float *const m_sh = reinterpret_cast<float *>(smem + C::ML_OFF), *const l_sh = m_sh + NW * ROWS;
     float *const factor = l_sh + NW * ROWS;
+    float *const ex_o = reinterpret_cast<float *>(smem + C::EX_OFF);
+    float2 *const ex_ml = reinterpret_cast<float2 *>(ex_o + ROWS * DP);
 
-    const Span sp = find_span<NT>(a, cta, scan_sh, &cur_sh);
-    Cursor cur = cur_sh;
-    if (tid == 0) write_record(a, sp, cur, cta);
+    Cursor cur;
+    int share = 0, shares = 1;
+    if (CL) {
+        shares = cluster_size();
+        share = cluster_rank();
+        const int item = cta / shares, m = row_tiles({0, a.n, 0, true}, a.G, a.rows);
+        cur.h = item % a.c.H;
+        cur.rt = item / a.c.H % m;
+        cur.b = item / a.c.H / m;
+        cur.s = load_seq(a, cur.b);
+        if (!cur.s.ok && tid == 0) flag_bad(a.status);
+        cur.k = 0;
+        cur.nt = cur.tiles_left = 1;
+    } else {
+        const Span sp = find_span<NT>(a, cta, scan_sh, &cur_sh);
+        cur = cur_sh;
+        if (tid == 0) write_record(a, sp, cur, cta);
+    }
 
     while (cur.tiles_left > 0) {
         const int k0 = cur.k, k1 = imin(cur.nt, cur.k + cur.tiles_left);
         const int seen = visible(cur.s, a.G, a.rows, cur.rt, a.causal);
-        const int end = imin(seen, k1 * kTile);                       // tokens of this piece
-        const int u0 = k0 * (kTile / 16), units = imax(0, (end + 15) / 16 - u0);
+        // tokens up to `end` and units from u0 on are this block's
+        int end, u0;
+        if (CL) {
+            const int all = (seen + 15) / 16;
+            u0 = (int)((int64_t)all * share / shares);
+            end = imin(seen, 16 * (int)((int64_t)all * (share + 1) / shares));
+        } else {
+            end = imin(seen, k1 * kTile);
+            u0 = k0 * (kTile / 16);
+        }
+        const int units = imax(0, (end + 15) / 16 - u0);
         const int mine = units > w ? (units - w + NW - 1) / NW : 0;   // this warp's units: u0 + w + i NW
         const int32_t *const row_table = a.c.table + (int64_t)cur.b * a.c.W;
         // ---- pages: lane i holds that of unit base + i of this warp -----------------
@@ -447,7 +510,10 @@ __global__ void __launch_bounds__(MmaCfg<DP, MT, F32>::NT, 2) attn_mma_kernel(co
 #pragma unroll
                 for (int y = 0; y < 4; ++y) v[y] = fmaf(f, join[(x * ROWS + r) * C::OS + 8 * (j + y) + n], v[y]);
             }
-            if (final) {
+            if (CL) {
+                *reinterpret_cast<float4 *>(&ex_o[r * DP + d]) = make_float4(v[0], v[1], v[2], v[3]);
+                if (d == 0) ex_ml[r] = make_float2(M, ls);
+            } else if (final) {
                 const float inv = ls == 0.f ? 0.f : 1.f / ls;
                 store_o4(a, F32 || a.o_f32, p.o + d, make_float4(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv));
                 if (a.L && d == 0) a.L[p.l] = ls == 0.f ? -INFINITY : (M + log2f(ls)) * kLn2;
@@ -456,6 +522,32 @@ __global__ void __launch_bounds__(MmaCfg<DP, MT, F32>::NT, 2) attn_mma_kernel(co
                 if (d == 0) a.part_ml[slot * a.rows + r] = make_float2(M, ls);
             }
         }
+        if (CL) {
+            cluster_sync();
+            // the blocks share the rows' channels out among them
+            for (int i = tid * shares + share; i < rows * (DP / 4); i += NT * shares) {
+                const int r = i / (DP / 4), d = (i % (DP / 4)) * 4;
+                if (d >= D) continue;
+                const RowPlace p = row_place(a, cur.s, cur.b, cur.rt, cur.h, r);
+                const uint32_t ml = tc::smem_u32(&ex_ml[r]), at = tc::smem_u32(&ex_o[r * DP + d]);
+                float M = kNoMax, ls = 0.f;
+                float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+                for (int x = 0; x < shares; ++x) M = fmaxf(M, ld_peer2(ml, x).x);
+                for (int x = 0; x < shares; ++x) {
+                    const float2 y = ld_peer2(ml, x);
+                    const float4 o4 = ld_peer4(at, x);
+                    const float f = y.y == 0.f ? 0.f : tc::ex2(y.x - M);
+                    ls = fmaf(f, y.y, ls);
+                    v.x = fmaf(f, o4.x, v.x); v.y = fmaf(f, o4.y, v.y);
+                    v.z = fmaf(f, o4.z, v.z); v.w = fmaf(f, o4.w, v.w);
+                }
+                const float inv = ls == 0.f ? 0.f : 1.f / ls;
+                store_o4(a, F32 || a.o_f32, p.o + d, make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv));
+                if (a.L && d == 0) a.L[p.l] = ls == 0.f ? -INFINITY : (M + log2f(ls)) * kLn2;
+            }
+            cluster_sync();                          // no block leaves while another reads it
+            return;
+        }
         __syncthreads();                             // the joining buffer is the next piece's ring
         cur.tiles_left -= k1 - k0;
         if (cur.tiles_left > 0) next_item(a, cur);
@@ -463,26 +555,46 @@ __global__ void __launch_bounds__(MmaCfg<DP, MT, F32>::NT, 2) attn_mma_kernel(co
     tc::pdl_launch_dependents();
 }
 
-template <int DP, int MT, bool F32>
-cudaError_t launch_mma(const AttnArgs &a, cudaStream_t st) {
-    using C = MmaCfg<DP, MT, F32>;
-    auto k = attn_mma_kernel<DP, MT, F32>;
-    const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::BYTES);
+template <int DP, int MT, bool F32, bool CL>
+cudaError_t launch_as(const AttnArgs &a, int grid, int cluster, cudaStream_t st) {
+    using C = MmaCfg<DP, MT, F32, CL>;
+    auto k = attn_mma_kernel<DP, MT, F32, CL>;
+    static SharedMemoryLimit limit;
+    cudaError_t e = limit.raise((const void *)k, (int)C::BYTES);
     if (e != cudaSuccess) return e;
-    k<<<a.grid, C::NT, C::BYTES, st>>>(a);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)grid);
+    cfg.blockDim = dim3(C::NT);
+    cfg.dynamicSmemBytes = C::BYTES;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)cluster;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = CL ? 1 : 0;
+    e = cudaLaunchKernelEx(&cfg, k, a);
     note_launch();
-    return cudaGetLastError();
+    return e == cudaSuccess ? cudaGetLastError() : e;
+}
+template <int DP, int MT, bool F32>
+cudaError_t launch_mma(const AttnArgs &a, int cluster, cudaStream_t st) {
+    if (cluster > 1) {
+        const int64_t items = (int64_t)a.c.B * a.c.H * row_tiles({0, a.n, 0, true}, a.G, a.rows);
+        return launch_as<DP, MT, F32, true>(a, (int)items * cluster, cluster, st);
+    }
+    return launch_as<DP, MT, F32, false>(a, a.grid, 1, st);
 }
 
 }  // namespace
 
-cudaError_t launch_attn_mma(const AttnArgs &a, bool bf16, cudaStream_t st) {
+cudaError_t launch_attn_mma(const AttnArgs &a, bool bf16, int cluster, cudaStream_t st) {
     const bool wide = a.c.D > 64, two = a.rows == 32;
     if (bf16) {
-        if (wide) return two ? launch_mma<128, 2, false>(a, st) : launch_mma<128, 1, false>(a, st);
-        return two ? launch_mma<64, 2, false>(a, st) : launch_mma<64, 1, false>(a, st);
+        if (wide) return two ? launch_mma<128, 2, false>(a, cluster, st) : launch_mma<128, 1, false>(a, cluster, st);
+        return two ? launch_mma<64, 2, false>(a, cluster, st) : launch_mma<64, 1, false>(a, cluster, st);
     }
-    return wide ? launch_mma<128, 1, true>(a, st) : launch_mma<64, 1, true>(a, st);
+    return wide ? launch_mma<128, 1, true>(a, cluster, st) : launch_mma<64, 1, true>(a, cluster, st);
 }
 
 }  // namespace cache

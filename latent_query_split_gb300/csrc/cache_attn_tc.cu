@@ -137,7 +137,7 @@ struct Piece {
 
 template <int D, int RT>
 __global__ void __launch_bounds__(512, 1)
-attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const AttnArgs a) {
+attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const __grid_constant__ AttnArgs a) {
     using C = TcCfg<D, RT>;
     constexpr int KSTG = C::KSTG, VSTG = C::VSTG, NSC = C::NSC;
     constexpr bool SEP = C::SEP;
@@ -776,7 +776,8 @@ cudaError_t launch_tc(const AttnArgs &a, cudaStream_t st) {
         !make_page_map(&mv, a.c.v, a.c, CU_TENSOR_MAP_SWIZZLE_NONE))
         return cudaErrorInvalidValue;
     auto k = attn_tc_kernel<D, RT>;
-    cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::ALLOC);
+    static SharedMemoryLimit limit;
+    const cudaError_t e = limit.raise((const void *)k, (int)C::ALLOC);
     if (e != cudaSuccess) return e;
     k<<<a.grid, C::THREADS, C::ALLOC, st>>>(mk, mv, a);
     note_launch();

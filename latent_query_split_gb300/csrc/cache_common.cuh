@@ -5,6 +5,8 @@
 #include "cache_plan.cuh"
 #include "flare_internal.cuh"
 
+#include <atomic>
+
 namespace flare {
 namespace cache {
 
@@ -65,12 +67,28 @@ enum class AttnKernel { kSimt, kMma, kTc };
 struct AttnPlan {
     AttnKernel kernel;
     int rows, grid;
+    int cluster;                        // blocks an item where the call takes one launch (1: spans and a merge)
     size_t part_ml, rec, bytes;         // workspace: part_O at 0
 };
-AttnPlan attn_plan(const Pool &c, int G, bool bf16, int64_t T, int family, int sms);
+AttnPlan attn_plan(const Pool &c, int G, bool bf16, int64_t T, bool ragged, int family, int sms);
 
-cudaError_t launch_attn(const AttnArgs &a, AttnKernel kernel, bool bf16, cudaStream_t st);
-cudaError_t launch_attn_mma(const AttnArgs &a, bool bf16, cudaStream_t st);
+// Allows kernel `f` `bytes` of dynamic shared memory, once for each device.
+struct SharedMemoryLimit {
+    std::atomic<uint64_t> done{0};
+    cudaError_t raise(const void *f, int bytes) {
+        int dev = 0;
+        cudaError_t e = cudaGetDevice(&dev);
+        if (e != cudaSuccess) return e;
+        const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+        if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+        e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+        if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+        return e;
+    }
+};
+
+cudaError_t launch_attn(const AttnArgs &a, const AttnPlan &plan, bool bf16, cudaStream_t st);
+cudaError_t launch_attn_mma(const AttnArgs &a, bool bf16, int cluster, cudaStream_t st);
 cudaError_t launch_attn_tc(const AttnArgs &a, cudaStream_t st);
 cudaError_t launch_append(const AppendArgs &a, bool bf16, cudaStream_t st);
 
