@@ -12,13 +12,19 @@
 //               for smaller ones. Two 8-bit products take as long as one of 16
 //               bits, and K is neither converted nor written a second time.
 //   w = 2^(S factor ks + ev - m)  one row a thread; ks = the page's key scale, 2^ev
-//               its value scale, m a reference at most 15 below the row's
-//               largest exponent, moved (with O and l) only when that is passed.
-//   O += w V    kind::f16: w in fp16 from TMEM (in place of S), V converted to
-//               fp16 (exact) by four warps into MN-major tiles. Rows of V that no
-//               token stands behind are written as zeros there: a cache's unused
-//               slots may hold NaN codes, and 0 * NaN is not 0.
-//   l += 2^-ev sum w.
+//               its value scale, m a reference that lies 90 below the row's largest
+//               exponent when it is set, and is moved (with O and l) only when a
+//               weight passes 2^122: next to never.
+//   O += w V    kind::f16: w in bf16 from TMEM, V converted to bf16 by four warps
+//               into MN-major tiles. Of bf16 for the range: with fp16 weights (2^-11
+//               instead of 2^-8 at most off) the references of rows that meet larger
+//               and larger scores had to move again and again, which took a quarter of
+//               the time, and products could not begin before a tile's last weight.
+//               A code is exact in bf16; its exponent is taken over as it is from fp16,
+//               which makes V smaller by 2^112 and w makes up for it. Rows of V that no
+//               token stands behind are written as zeros there: a cache's unused slots
+//               may hold NaN codes, and 0 * NaN is not 0.
+//   l += 2^(-ev - 64) sum w  (in range for every ev).
 //
 // Roles (16 warps): 0 fetches pages and scales, 1 issues O += w V, 2 issues S
 // (two issuers: the waits of one run under the other's products), 3 is idle, 4-7
@@ -41,10 +47,13 @@ namespace {
 using namespace tc;
 
 constexpr float kNoMax = -3.0e38f;
-constexpr float kMaxSum = 60000.f;       // of 16 weights: fp16 holds 65504
-constexpr float kOver = 11.5f;           // the largest exponent of such a sum is over this
-constexpr int kTries = 1 << 23;          // of a wait: a second at least
-constexpr float kFresh = 8.f;            // a new largest weight is 2^8 at most
+constexpr float kMaxSum = 8.5e37f;       // 2^126, of 16 weights
+constexpr float kOver = 121.f;           // the largest exponent of such a sum is over this
+constexpr float kFresh = 90.f;           // where a row's largest exponent is put
+constexpr float kSumShift = 64.f;        // l is smaller by 2^64 than the sum of the weights
+constexpr float kOutScale = 0x1p48f;     // 2^(112 - 64): V's exponents over l's shift
+constexpr int kPub = 2;                  // a unit's weights are handed on in two halves (1: at once)
+constexpr int kTries = 1 << 20;          // of a wait: far longer than any that ends
 
 template <int D_, int RT_>
 struct TcCfg {
@@ -65,21 +74,21 @@ struct TcCfg {
     static constexpr uint32_t K_OFF = Q_OFF + RT * 2 * TILE8;
     static constexpr uint32_t V8_OFF = K_OFF + KSTG * TILE8;
     static constexpr uint32_t V16_OFF = V8_OFF + VSTG * TILE8;
-    static constexpr uint32_t SC_OFF = V16_OFF + 2 * TILE16;           // [NSC][8] {ks, ev, 1 / vs, valid}
+    static constexpr uint32_t SC_OFF = V16_OFF + 2 * TILE16;           // [NSC][8] {ks, ev, 2^(-ev - 64), valid}
     static constexpr uint32_t FAC_OFF = SC_OFF + NSC * 8 * 16;         // [ROWS] row factors
     static constexpr uint32_t STAT_OFF = FAC_OFF + ROWS * 4;           // RT = 1: [2][128] (m, l)
     static constexpr uint32_t BAR_OFF = STAT_OFF + (RT == 1 ? 2048 : 0);
-    static constexpr int NBAR = 2 * KSTG + 2 * VSTG + NSC + 4 + 2 + 6 + 2 + 3;
+    static constexpr int NBAR = 2 * KSTG + 2 * VSTG + NSC + 4 + 2 + 4 + 2 * kPub + 4 + 3;
     static constexpr uint32_t MISC_OFF = BAR_OFF + NBAR * 8;
     static constexpr uint32_t BYTES = MISC_OFF + 16;
     static constexpr uint32_t ALLOC = BYTES + 1024;
     static_assert(ALLOC <= 232448, "shared memory budget of one CTA exceeded");
 };
 
-__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
-    uint32_t r;
-    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    return r;
+// Two fp16 numbers of 4 significant bits as bf16, 2^-112 times as large: sign, then
+// fp16's five bits of exponent in the low five of bf16's eight, then the mantissa.
+__device__ __forceinline__ uint32_t low_bf16x2(uint32_t h) {
+    return (h & 0x80008000u) | ((h >> 3) & 0x0fff0fffu);
 }
 __device__ __forceinline__ uint32_t pack_e4m3(float lo, float hi) {
     uint16_t r;
@@ -155,7 +164,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
     };
     const uint32_t k_full = bars(KSTG), k_empty = bars(KSTG), v_full = bars(VSTG), v_empty = bars(VSTG), sc_full = bars(NSC),
                    h_full = bars(2), h_empty = bars(2), q_full = bars(1), q_read = bars(1), s_full = bars(2),
-                   s_free = bars(2), p_full = bars(2), o_done = bars(2), soft = bars(1), drain = bars(2);
+                   s_free = bars(2), p_full = bars(2 * kPub), o_done = bars(2), o_half = bars(2), soft = bars(1), drain = bars(2);
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::MISC_OFF);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + C::MISC_OFF + 4);
     const float4 *const sc_sh = reinterpret_cast<const float4 *>(smem + C::SC_OFF);
@@ -183,8 +192,9 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
             mbar_init(h_empty + 8 * s, 1);
             mbar_init(s_full + 8 * s, 1);
             mbar_init(s_free + 8 * s, SEP ? 4 : 1);  // the group's warps, or a commit
-            mbar_init(p_full + 8 * s, 4);
+            for (int h = 0; h < kPub; ++h) mbar_init(p_full + 8 * (s * kPub + h), 4);
             mbar_init(o_done + 8 * s, 1);
+            mbar_init(o_half + 8 * s, 1);
         }
         mbar_init(drain, 1);
         mbar_init(drain + 8, 1);
@@ -264,7 +274,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
                         if (mine) {
                             const int ex = (int)((__float_as_uint(vs) >> 23) & 0xff);
                             *reinterpret_cast<float4 *>(smem + C::SC_OFF + (scl * 8 + grp) * 16) =
-                                page >= 0 ? make_float4(ks, (float)(ex - 127), __int_as_float((254 - ex) << 23), 1.f)
+                                page >= 0 ? make_float4(ks, (float)(ex - 127), __int_as_float((254 - 64 - ex) << 23), 1.f)
                                           : make_float4(1.f, 0.f, 0.f, 0.f);
                         }
                         __syncwarp();
@@ -340,7 +350,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
             __syncwarp();
         } else if (warp == 1) {
             // ---------------- O += w V ----------------
-            constexpr uint32_t idPV = idesc_f16(128, D, 0, 1);
+            constexpr uint32_t idPV = idesc_bf16(128, D, 0, 1);
             int j = 0, q = 0;
             bool ok = true;
 #pragma unroll 1
@@ -353,16 +363,27 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
                     for (int u = 0; u < RT; ++u, ++q) {
                         const int g = q & 1;
                         if (u == 0 && !(ok = wwait(h_full + 8 * (j & 1), (uint32_t)(j >> 1) & 1))) break;
-                        if (!(ok = wwait(p_full + 8 * g, (uint32_t)(q >> 1) & 1))) break;
-                        tc_fence_after();
                         const uint32_t tP = tmem + (SEP ? C::P_COL + g * 64 : g * 128);
+                        // half after half, the first one's products under the second one's exponentials
+#pragma unroll 1
+                        for (int h = 0; h < kPub; ++h) {
+                            if (!(ok = wwait(p_full + 8 * (g * kPub + h), (uint32_t)(q >> 1) & 1))) break;
+                            tc_fence_after();
 #pragma unroll
-                        for (int kb = 0; kb < 8; ++kb)
-                            umma_ts_elect(tmem + C::O_COL + g * D, tP + kb * 8, dV + (uint64_t)(kb * 16 * 128 >> 4), idPV,
-                                          kb > 0 || !fresh[g]);
+                            for (int kb = 0; kb < 8 / kPub; ++kb) {
+                                const int at = h * (8 / kPub) + kb;
+                                umma_ts_elect(tmem + C::O_COL + g * D, tP + at * 8, dV + (uint64_t)(at * 16 * 128 >> 4), idPV,
+                                              at > 0 || !fresh[g]);
+                            }
+                            if (h < kPub - 1) {
+                                umma_commit_elect(o_half + 8 * g);
+                            } else {
+                                if (!SEP) umma_commit_elect(s_free + 8 * g);
+                                umma_commit_elect(o_done + 8 * g);
+                            }
+                        }
+                        if (!ok) break;
                         fresh[g] = false;
-                        if (!SEP) umma_commit_elect(s_free + 8 * g);
-                        umma_commit_elect(o_done + 8 * g);
                     }
                     if (ok) umma_commit_elect(h_empty + 8 * (j & 1));
                 }
@@ -466,10 +487,10 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
                     for (int i = 0; i < 4; ++i) {
                         const int r = r0 + (i0 + i) * (128 / CH);
                         if (!whole && !(r < left && sc_sh[(j % NSC) * 8 + (r >> 4)].w != 0.f)) v[i] = make_uint4(0, 0, 0, 0);
-                        const uint4 lo = make_uint4(f16x2_of_e4m3x2(v[i].x), f16x2_of_e4m3x2_hi(v[i].x),
-                                                    f16x2_of_e4m3x2(v[i].y), f16x2_of_e4m3x2_hi(v[i].y));
-                        const uint4 hi = make_uint4(f16x2_of_e4m3x2(v[i].z), f16x2_of_e4m3x2_hi(v[i].z),
-                                                    f16x2_of_e4m3x2(v[i].w), f16x2_of_e4m3x2_hi(v[i].w));
+                        const uint4 lo = make_uint4(low_bf16x2(f16x2_of_e4m3x2(v[i].x)), low_bf16x2(f16x2_of_e4m3x2_hi(v[i].x)),
+                                                    low_bf16x2(f16x2_of_e4m3x2(v[i].y)), low_bf16x2(f16x2_of_e4m3x2_hi(v[i].y)));
+                        const uint4 hi = make_uint4(low_bf16x2(f16x2_of_e4m3x2(v[i].z)), low_bf16x2(f16x2_of_e4m3x2_hi(v[i].z)),
+                                                    low_bf16x2(f16x2_of_e4m3x2(v[i].w)), low_bf16x2(f16x2_of_e4m3x2_hi(v[i].w)));
                         const uint32_t row = dst + (c >> 2) * (128 * 128) + r * 128;
                         sts16(row + (((cc + first) ^ (r & 7)) << 4), first ? hi : lo);
                         sts16(row + (((cc + 1 - first) ^ (r & 7)) << 4), first ? lo : hi);
@@ -510,9 +531,6 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
             const int lim = p.valid ? p.limit : seen;
             const int min_lim = imin(__reduce_min_sync(0xffffffffu, lim), seen);
             const bool idle = !__any_sync(0xffffffffu, p.valid);
-            // where a new largest weight starts: the fp16 weights that round to zero, under
-            // 2^-25, stay 2^-10 of the largest together, however many tokens a row sees
-            const float fresh_at = fminf(fmaxf((float)(32 - __clz(seen)) - 15.f, 0.f), kFresh);
             float m = kNoMax, l = 0.f;
             bool has = false;
 #pragma unroll 1
@@ -528,7 +546,8 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
                 tc_fence_after();
                 if (idle) {                                     // no row of this warp is anyone's
                     if (SEP && lane == 0) mbar_arrive(s_free + 8 * g);
-                    if (lane == 0) mbar_arrive(p_full + 8 * g);
+                    if (lane == 0)
+                        for (int h = 0; h < kPub; ++h) mbar_arrive(p_full + 8 * (g * kPub + h));
                     has = true;
                     ++units;
                     continue;
@@ -558,7 +577,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
                         }
                     }
                     tmem_wait_st();
-                    if (m == kNoMax && best != -INFINITY) m = best - fresh_at;
+                    if (m == kNoMax && best != -INFINITY) m = best - kFresh;
                 }
                 // The row's 128 products, 32 at a time: exponents against the reference as it is,
                 // the next products on their way, weights, their sums by page group. No pass for
@@ -585,7 +604,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
                         for (int i = 0; i < 8; ++i) {
                             const float p0 = ex2(u[16 * h + 2 * i]), p1 = ex2(u[16 * h + 2 * i + 1]);
                             s2 = i == 0 ? f2pack(p0, p1) : add2(s2, f2pack(p0, p1));
-                            w[8 * h + i] = pack_f16(p0, p1);
+                            w[8 * h + i] = pack_bf16(p0, p1);
                         }
                         float s0, s1;
                         f2unpack(s2, s0, s1);
@@ -595,6 +614,12 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
                 auto place = [&](int c) {
                     l = fmaf(s[0], sc[2 * c].z, fmaf(s[1], sc[2 * c + 1].z, l));
                     tmem_st16(p_tmem + 16 * c, w);
+                    if ((c + 1) % (4 / kPub) == 0) {
+                        tmem_wait_st();
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(p_full + 8 * (g * kPub + c / (4 / kPub)));
+                    }
                 };
                 int from = 4;                                   // products that the slow loop takes
                 tmem_ld32(s_tmem, x);
@@ -614,10 +639,6 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
                 }
                 if (!ok) break;
                 if (__builtin_expect(from < 4, 0)) {
-                    if (has) {
-                        if (!(ok = wwait(o_done + 8 * g, (uint32_t)(units - 1) & 1))) break;
-                        tc_fence_after();
-                    }
 #pragma unroll 1
                     for (int c = from; c < 4; ++c) {
                         tmem_wait_ld();
@@ -629,29 +650,32 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
                         for (int i = 1; i < 32; ++i) top = fmaxf(top, u[i]);
                         const bool over = top > kOver;
                         if (__any_sync(0xffffffffu, over)) {
-                            // The references of the rows that need it move by whole powers of two:
-                            // O, l and the weights of this tile that are in place are scaled without
-                            // a rounding (but of what becomes subnormal).
-                            const float by = over ? ceilf(top) - fresh_at : 0.f;
+                            // The references of the rows that need it move by whole powers of two: O,
+                            // l and the weights of this tile that are not handed on yet are scaled
+                            // without a rounding (but of what becomes subnormal). What is handed on
+                            // is in O once its products are done.
+                            const float by = over ? ceilf(top) - kFresh : 0.f;
                             const float f = ex2(-by);
-                            const __half2 hf = __float2half2_rn(f);
                             m += by;
                             l *= f;
 #pragma unroll
                             for (int i = 0; i < 32; ++i) u[i] -= by;
                             tmem_wait_st();
+                            const int done = c / (4 / kPub);                 // parts handed on
 #pragma unroll 1
-                            for (int d = 0; d < c; ++d) {
+                            for (int d = done * (4 / kPub); d < c; ++d) {
                                 tmem_ld16(p_tmem + 16 * d, w);
                                 tmem_wait_ld();
 #pragma unroll
-                                for (int i = 0; i < 16; ++i) {
-                                    const __half2 y = __hmul2(*reinterpret_cast<__half2 *>(&w[i]), hf);
-                                    w[i] = *reinterpret_cast<const uint32_t *>(&y);
-                                }
+                                for (int i = 0; i < 16; ++i)
+                                    w[i] = pack_bf16(__uint_as_float(w[i] << 16) * f, __uint_as_float(w[i] & 0xffff0000u) * f);
                                 tmem_st16(p_tmem + 16 * d, w);
                             }
-                            if (has) {
+                            if (has || done > 0) {
+                                if (!(ok = done > 0 ? wwait(o_half + 8 * g, (uint32_t)units & 1)
+                                                    : wwait(o_done + 8 * g, (uint32_t)(units - 1) & 1)))
+                                    break;
+                                tc_fence_after();
 #pragma unroll 1
                                 for (int d = 0; d < D / 32; ++d) {
                                     tmem_ld32(o_tmem + d * 32, x);
@@ -665,16 +689,13 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
                         weights();
                         place(c);
                     }
+                    if (!ok) break;
                 }
                 if (SEP) {
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(s_free + 8 * g);          // the scores may be overwritten
                 }
-                tmem_wait_st();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(p_full + 8 * g);
                 has = true;
                 ++units;
             }
@@ -698,7 +719,9 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
                 c1 = s1.y == 0.f ? 0.f : ex2(s1.x - M);
                 ls = (c0 != 0.f ? c0 * s0.y : 0.f) + (c1 != 0.f ? c1 * s1.y : 0.f);
             }
-            const float inv = !final ? 1.f : ls == 0.f ? 0.f : 1.f / ls;
+            // (O is smaller by 2^112 and l by 2^64 than the sums)
+            const float inv = !final ? kOutScale : ls == 0.f ? 0.f : kOutScale / ls;
+            M += kSumShift;
             c0 *= inv;
             c1 *= inv;
             const bool wide_o = !a.o_f32 && (reinterpret_cast<uintptr_t>(reinterpret_cast<__nv_bfloat16 *>(a.O) + p.o) & 15) == 0;
