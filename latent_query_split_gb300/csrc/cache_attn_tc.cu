@@ -20,8 +20,8 @@
 //               instead of 2^-8 at most off) the references of rows that meet larger
 //               and larger scores had to move again and again, which took a quarter of
 //               the time, and products could not begin before a tile's last weight.
-//               A code is exact in bf16; its exponent is taken over as it is from fp16,
-//               which makes V smaller by 2^112 and w makes up for it. Rows of V that no
+//               A code is exact in bf16; its exponent bits are taken over as they
+//               are, which makes V smaller by 2^120, and w makes up for it. Rows of V that no
 //               token stands behind are written as zeros there: a cache's unused slots
 //               may hold NaN codes, and 0 * NaN is not 0.
 //   l += 2^(-ev - 64) sum w  (in range for every ev).
@@ -51,7 +51,7 @@ constexpr float kMaxSum = 8.5e37f;       // 2^126, of 16 weights
 constexpr float kOver = 121.f;           // the largest exponent of such a sum is over this
 constexpr float kFresh = 90.f;           // where a row's largest exponent is put
 constexpr float kSumShift = 64.f;        // l is smaller by 2^64 than the sum of the weights
-constexpr float kOutScale = 0x1p48f;     // 2^(112 - 64): V's exponents over l's shift
+constexpr float kOutScale = 0x1p56f;     // 2^(120 - 64): V's exponents over l's shift
 constexpr int kPub = 2;                  // a unit's weights are handed on in two halves (1: at once)
 constexpr int kTries = 1 << 20;          // of a wait: far longer than any that ends
 
@@ -85,10 +85,13 @@ struct TcCfg {
     static_assert(ALLOC <= 232448, "shared memory budget of one CTA exceeded");
 };
 
-// Two fp16 numbers of 4 significant bits as bf16, 2^-112 times as large: sign, then
-// fp16's five bits of exponent in the low five of bf16's eight, then the mantissa.
-__device__ __forceinline__ uint32_t low_bf16x2(uint32_t h) {
-    return (h & 0x80008000u) | ((h >> 3) & 0x0fff0fffu);
+// Four e4m3 codes as bf16 numbers 2^-120 times as large: sign, then the code's
+// four bits of exponent in the low four of bf16's eight, then its mantissa (a
+// subnormal code becomes a subnormal number of the same value). Seven operations
+// on the four of them: the high bytes, the low bytes, and two interleavings.
+__device__ __forceinline__ uint2 bf16x4_of(uint32_t codes) {
+    const uint32_t high = (codes & 0x80808080u) | ((codes >> 4) & 0x07070707u), low = (codes << 4) & 0xf0f0f0f0u;
+    return make_uint2(__byte_perm(low, high, 0x5140), __byte_perm(low, high, 0x7362));
 }
 __device__ __forceinline__ uint32_t pack_e4m3(float lo, float hi) {
     uint16_t r;
@@ -487,10 +490,8 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
                     for (int i = 0; i < 4; ++i) {
                         const int r = r0 + (i0 + i) * (128 / CH);
                         if (!whole && !(r < left && sc_sh[(j % NSC) * 8 + (r >> 4)].w != 0.f)) v[i] = make_uint4(0, 0, 0, 0);
-                        const uint4 lo = make_uint4(low_bf16x2(f16x2_of_e4m3x2(v[i].x)), low_bf16x2(f16x2_of_e4m3x2_hi(v[i].x)),
-                                                    low_bf16x2(f16x2_of_e4m3x2(v[i].y)), low_bf16x2(f16x2_of_e4m3x2_hi(v[i].y)));
-                        const uint4 hi = make_uint4(low_bf16x2(f16x2_of_e4m3x2(v[i].z)), low_bf16x2(f16x2_of_e4m3x2_hi(v[i].z)),
-                                                    low_bf16x2(f16x2_of_e4m3x2(v[i].w)), low_bf16x2(f16x2_of_e4m3x2_hi(v[i].w)));
+                        const uint2 y0 = bf16x4_of(v[i].x), y1 = bf16x4_of(v[i].y), y2 = bf16x4_of(v[i].z), y3 = bf16x4_of(v[i].w);
+                        const uint4 lo = make_uint4(y0.x, y0.y, y1.x, y1.y), hi = make_uint4(y2.x, y2.y, y3.x, y3.y);
                         const uint32_t row = dst + (c >> 2) * (128 * 128) + r * 128;
                         sts16(row + (((cc + first) ^ (r & 7)) << 4), first ? hi : lo);
                         sts16(row + (((cc + 1 - first) ^ (r & 7)) << 4), first ? lo : hi);
@@ -719,7 +720,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
                 c1 = s1.y == 0.f ? 0.f : ex2(s1.x - M);
                 ls = (c0 != 0.f ? c0 * s0.y : 0.f) + (c1 != 0.f ? c1 * s1.y : 0.f);
             }
-            // (O is smaller by 2^112 and l by 2^64 than the sums)
+            // (O is smaller by 2^120 and l by 2^64 than the sums)
             const float inv = !final ? kOutScale : ls == 0.f ? 0.f : kOutScale / ls;
             M += kSumShift;
             c0 *= inv;

@@ -137,6 +137,9 @@ def freqs(rot, base=10000.0):
     return (base ** (-torch.arange(0, rot, 2, dtype=torch.float64) / rot)).float().cuda() if rot else None
 
 
+# Calls of few tokens a sequence, of many (a page and some heads a block: one, two
+# and four tasks a thread, several heads at once), and of rotations whose pairs do
+# not lie in runs of eight.
 APPENDS = [  # dtype, H, Hq, D, page, rot, interleaved, lens, counts
     ("bf16", 2, 4, 64, 16, 64, False, [0, 5, 16, 31], [1, 1, 1, 1]),
     ("bf16", 1, 3, 128, 64, 128, False, [0, 63, 64, 100], [70, 1, 0, 129]),
@@ -148,6 +151,13 @@ APPENDS = [  # dtype, H, Hq, D, page, rot, interleaved, lens, counts
     ("fp32", 1, 5, 112, 128, 112, False, [200, 0], [1, 2]),
     ("fp32", 4, 0, 128, 64, 100, False, [64] * 5, [0, 0, 3, 0, 61]),
     ("bf16", 8, 32, 128, 64, 128, True, [63, 0], [130, 5]),
+    ("bf16", 3, 9, 128, 128, 64, False, [100, 0], [400, 129]),
+    ("fp32", 2, 4, 128, 128, 128, True, [5], [260]),
+    ("bf16", 5, 5, 32, 16, 32, False, [9, 0, 16], [40, 33, 100]),
+    ("bf16", 9, 0, 64, 16, 16, True, [15, 0], [90, 17]),
+    ("fp32", 3, 6, 80, 32, 80, False, [31, 1], [70, 64]),
+    ("bf16", 2, 18, 128, 32, 128, False, [31, 0, 5], [2, 1, 4]),
+    ("fp32", 9, 9, 96, 16, 32, True, [15, 3], [1, 8]),
 ]
 
 
@@ -180,6 +190,24 @@ def test_append_equal_rows_from_a_fused_projection():
     lens_out, q_out = flare.flare_cache_append(cache, K, V, ints(lens), Q=Q, inv_freq=f)
     flat = lambda y: y.reshape(B * n, *y.shape[2:])  # noqa: E731
     check_append(cache, before, flat(K), flat(V), flat(Q), lens, [n] * B, f, False, lens_out, q_out)
+
+
+@pytest.mark.parametrize("n", [2, 40])
+def test_append_of_any_alignment(n):
+    """Tensors that begin at odd elements."""
+    H, Hq, D, page, lens = 2, 4, 64, 16, [14]
+    cache = make_cache(1, 5, H, D, page)
+    fill(cache, lens, seed=13)
+    before = cache_ref.host(cache)
+    g = torch.Generator().manual_seed(14)
+    off = lambda heads: torch.randn(n * heads * D + 1, generator=g).bfloat16().cuda()[1:].view(1, n, heads, D)  # noqa: E731
+    K, V, Q, f = off(H), off(H), off(Hq), freqs(D)
+    out, q = flare.flare_cache_append(cache, K, V, ints(lens), Q=Q, inv_freq=f)
+    check_append(cache, before, K[0], V[0], Q[0], lens, [n], f, False, out, q[0])
+    O = off(Hq)
+    flare.flare_cache_attn(Q, cache, out, O=O)
+    L = flare.flare_cache_attn(Q, cache, out)[1]
+    check_attn(O[0], L[0], Q[0], cache, out.tolist(), [n], True)
 
 
 @pytest.mark.parametrize("at", [0, 1000, 999_999, (1 << 30) - 200])
@@ -220,13 +248,18 @@ def test_append_grows_a_pages_scale():
         check_append(cache, before, K, V, None, [i], [1], None, False, out, None)
 
 
-def test_append_holds_what_is_not_finite_as_nan_keys():
+@pytest.mark.parametrize("pieces", [[20], [4, 3, 10, 3]])
+def test_append_holds_what_is_not_finite_as_nan_keys(pieces):
     cache = make_cache(1, 2, 2, 64, 16)
     K, V = (torch.randn((20, 2, 64), generator=torch.Generator().manual_seed(s)).bfloat16() for s in (8, 9))
     K[3, 0, 5], K[4, 1, 0], V[6, 0, 63], V[17, 1, 1] = math.nan, math.inf, -math.inf, math.nan
-    before = cache_ref.host(cache)
-    out, _ = run_append(cache, K.cuda(), V.cuda(), None, [0], [20], freqs(64))
-    check_append(cache, before, K, V, None, [0], [20], freqs(64), False, out, None)
+    at = 0
+    for n in pieces:
+        before = cache_ref.host(cache)
+        k, v = K[at:at + n], V[at:at + n]
+        out, _ = run_append(cache, k.cuda(), v.cuda(), None, [at], [n], freqs(64))
+        check_append(cache, before, k, v, None, [at], [n], freqs(64), False, out, None)
+        at += n
     assert not cache.v.float()[cache.page_table[0].long()].transpose(1, 2).reshape(32, 2, 64)[:20].isnan().any()
     Q = torch.randn((20, 2, 64), generator=torch.Generator().manual_seed(10)).bfloat16().cuda()
     for kernel in ("simt", "auto"):
@@ -344,6 +377,32 @@ def test_attn(kernel, dtype, H, G, D, page, lens, counts, causal):
         x.check(name)
 
 
+EQUAL = [  # dtype, H, G, D, page, lens, n, causal: equal sequences (small ones are a cluster's)
+    ("bf16", 2, 4, 128, 64, [1500], 1, True),
+    ("bf16", 2, 5, 64, 16, [2, 900, 33, 128, 0, 17], 3, True),
+    ("bf16", 1, 3, 96, 32, [100, 1], 9, False),
+    ("bf16", 4, 8, 128, 128, [129] * 5, 4, True),
+    ("fp32", 2, 4, 64, 32, [1, 1200, 0, 300], 1, True),
+    ("fp32", 1, 9, 112, 16, [260, 500], 4, True),
+    ("bf16", 8, 2, 32, 16, [5000, 31, 700], 2, False),
+]
+
+
+@pytest.mark.parametrize("dtype,H,G,D,page,lens,n,causal", EQUAL)
+def test_attn_equal_sequences(dtype, H, G, D, page, lens, n, causal):
+    B = len(lens)
+    cache = make_cache(B, max(lens) // page + 2, H, D, page)
+    fill(cache, lens, seed=70)
+    Q = torch.randn((B, n, H * G, D), generator=torch.Generator().manual_seed(71)).to(DT[dtype]).cuda()
+    O, go = guarded(Q.shape, DT[dtype], fill=7.0)
+    L, gl = guarded(Q.shape[:-1], fill=7.0)
+    flare.flare_cache_attn(Q, cache, ints(lens), causal=causal, O=O, L=L)
+    flare.flare_device_status()
+    check_attn(O, L, Q.reshape(B * n, H * G, D), cache, lens, [n] * B, causal)
+    go.check("O")
+    gl.check("L")
+
+
 @pytest.mark.parametrize("kernel", ["simt", "auto"])
 @pytest.mark.parametrize("n", [1, 40, 140])
 def test_attn_equal_rows_strided_queries_and_scale(kernel, n):
@@ -443,6 +502,42 @@ def test_attn_skips_bad_pages_and_says_so(kernel, n):
     short = cache.page_table.clone()
     short[0, :-1] = cache.page_table[0, [0, 2, 3, 4, 5, 6, 7]]
     check_attn(O, L, Q, cache._replace(page_table=short), [84, 48, 128], [n] * B, False)
+
+
+@pytest.mark.parametrize("kernel", ["simt", "auto"])
+@pytest.mark.parametrize("D,n", [(64, 1), (128, 20), (64, 130), (128, 140)])
+def test_attn_every_code(kernel, D, n):
+    """Every finite code, subnormal ones too, as keys and as values: tokens of the
+    smallest codes alone, and of all of them."""
+    page, H = 32, 1
+    cache = make_cache(1, 9, H, D, page)
+    fill(cache, [256], seed=60)
+    codes = torch.tensor([c for c in range(256) if c & 0x7F != 0x7F], dtype=torch.uint8)
+    tiny = torch.tensor([1, 2, 3, 4, 5, 6, 7, 0x81, 0x82, 0x83, 0x85, 0x87, 0, 0x80], dtype=torch.uint8)
+    g = torch.Generator().manual_seed(61)
+    Q = torch.randn((n, H, D), generator=g).bfloat16().cuda()
+    for pick in (tiny, codes):
+        for x in (cache.k, cache.v):
+            b = x.view(torch.uint8)
+            b.copy_(pick[torch.randint(0, len(pick), b.shape, generator=g)])
+        O, L = flare.flare_cache_attn(Q, cache, ints([256]), cu_seqlens=ints([0, n]), causal=False, kernel=kernel)
+        check_attn(O, L, Q, cache, [256], [n], False, kernel=kernel)
+
+
+@pytest.mark.parametrize("kernel", ["simt", "auto"])
+@pytest.mark.parametrize("D,n", [(64, 1), (128, 40), (64, 130), (128, 300)])
+def test_attn_scores_that_grow(kernel, D, n):
+    """Keys that double from tile to tile: the largest score moves by more than any
+    reference leaves room for, inside a tile and from one to the next."""
+    page, H, lens = 32, 1, [1024]
+    cache = make_cache(1, 33, H, D, page)
+    fill(cache, lens, seed=62)
+    for w in range(32):
+        cache.k_scale[int(cache.page_table[0, w])] = 2.0 ** (w - 24)
+    for seed in (63, 64):
+        Q = torch.randn((n, H, D), generator=torch.Generator().manual_seed(seed)).bfloat16().cuda()
+        O, L = flare.flare_cache_attn(Q, cache, ints(lens), cu_seqlens=ints([0, n]), causal=False, kernel=kernel, scale=0.02)
+        check_attn(O, L, Q, cache, lens, [n], False, scale=0.02, kernel=kernel)
 
 
 @pytest.mark.parametrize("dtype,n", [("bf16", 1), ("bf16", 130), ("fp32", 1)])
