@@ -78,7 +78,7 @@ struct TcCfg {
     static constexpr uint32_t FAC_OFF = SC_OFF + NSC * 8 * 16;         // [ROWS] row factors
     static constexpr uint32_t STAT_OFF = FAC_OFF + ROWS * 4;           // RT = 1: [2][128] (m, l)
     static constexpr uint32_t BAR_OFF = STAT_OFF + (RT == 1 ? 2048 : 0);
-    static constexpr int NBAR = 2 * KSTG + 2 * VSTG + NSC + 4 + 2 + 4 + 2 * kPub + 4 + 3;
+    static constexpr int NBAR = 2 * KSTG + 2 * VSTG + 4 + 2 + 4 + 2 * kPub + 4 + 3;
     static constexpr uint32_t MISC_OFF = BAR_OFF + NBAR * 8;
     static constexpr uint32_t BYTES = MISC_OFF + 16;
     static constexpr uint32_t ALLOC = BYTES + 1024;
@@ -165,7 +165,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
         nbar += n;
         return b;
     };
-    const uint32_t k_full = bars(KSTG), k_empty = bars(KSTG), v_full = bars(VSTG), v_empty = bars(VSTG), sc_full = bars(NSC),
+    const uint32_t k_full = bars(KSTG), k_empty = bars(KSTG), v_full = bars(VSTG), v_empty = bars(VSTG),
                    h_full = bars(2), h_empty = bars(2), q_full = bars(1), q_read = bars(1), s_full = bars(2),
                    s_free = bars(2), p_full = bars(2 * kPub), o_done = bars(2), o_half = bars(2), soft = bars(1), drain = bars(2);
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::MISC_OFF);
@@ -189,11 +189,10 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
             mbar_init(v_full + 8 * s, 1);
             mbar_init(v_empty + 8 * s, 4);           // the converting warps
         }
-        for (int s = 0; s < NSC; ++s) mbar_init(sc_full + 8 * s, 1);
         for (int s = 0; s < 2; ++s) {
             mbar_init(h_full + 8 * s, 4);
             mbar_init(h_empty + 8 * s, 1);
-            mbar_init(s_full + 8 * s, 1);
+            mbar_init(s_full + 8 * s, 2);            // the products, and their issuer, which has seen the scales
             mbar_init(s_free + 8 * s, SEP ? 4 : 1);  // the group's warps, or a commit
             for (int h = 0; h < kPub; ++h) mbar_init(p_full + 8 * (s * kPub + h), 4);
             mbar_init(o_done + 8 * s, 1);
@@ -281,10 +280,8 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
                                           : make_float4(1.f, 0.f, 0.f, 0.f);
                         }
                         __syncwarp();
-                        if (lane == 0) {
-                            mbar_arrive(sc_full + 8 * scl);
-                            mbar_arrive_expect_tx(k_full + 8 * ksl, count * bytes);
-                        }
+                        // (what arrives on k_full and v_full releases the scales too)
+                        if (lane == 0) mbar_arrive_expect_tx(k_full + 8 * ksl, count * bytes);
                         __syncwarp();
                         if (load) tma_load_2d(sbase + C::K_OFF + ksl * C::TILE8 + grp * 16 * D, &tmK, 0, row, k_full + 8 * ksl);
                         __syncwarp();
@@ -340,6 +337,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
                             umma_f8_ss_elect(tmem + g * 128, dLo + 2 * kb, dK + 2 * kb, idLo, 1u);
                         }
                         umma_commit_elect(s_full + 8 * g);
+                        if (lane == 0) mbar_arrive(s_full + 8 * g);
                     }
                     if (ok) umma_commit_elect(k_empty + 8 * (j % KSTG));
                 }
@@ -470,7 +468,6 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
             for (int k = pc.k0; k < pc.k1 && ok; ++k, ++j) {
                 q += RT;
                 if (!(ok = wwait(v_full + 8 * (j % VSTG), (uint32_t)(j / VSTG) & 1))) break;
-                if (!(ok = wwait(sc_full + 8 * (j % NSC), (uint32_t)(j / NSC) & 1))) break;
                 if (j >= 2 && !(ok = wwait(h_empty + 8 * (j & 1), (uint32_t)((j >> 1) - 1) & 1))) break;
                 const int left = seen - k * kTile;
                 const uint32_t src = sbase + C::V8_OFF + (j % VSTG) * C::TILE8, dst = sbase + C::V16_OFF + (j & 1) * C::TILE16;
@@ -539,14 +536,14 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
                 if (RT == 1 && (j & 1) != g) continue;
                 const uint32_t s_tmem = tmem + g * 128 + lane_off;
                 const uint32_t p_tmem = SEP ? tmem + C::P_COL + g * 64 + lane_off : s_tmem;
-                if (!(ok = wwait(sc_full + 8 * (j % NSC), (uint32_t)(j / NSC) & 1))) break;
                 const float4 *const sc = sc_sh + (j % NSC) * 8;
                 const int n0 = k * kTile;
-                const bool whole = __all_sync(0xffffffffu, n0 + kTile <= min_lim && sc[lane & 7].w != 0.f);
                 if (!(ok = wwait(s_full + 8 * g, (uint32_t)units & 1))) break;
                 tc_fence_after();
                 if (idle) {                                     // no row of this warp is anyone's
                     if (SEP && lane == 0) mbar_arrive(s_free + 8 * g);
+                    // (its arrivals for this unit come after everyone's for the one before)
+                    if (has && !(ok = wwait(o_done + 8 * g, (uint32_t)(units - 1) & 1))) break;
                     if (lane == 0)
                         for (int h = 0; h < kPub; ++h) mbar_arrive(p_full + 8 * (g * kPub + h));
                     has = true;
@@ -554,6 +551,8 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
                     continue;
                 }
                 uint32_t x[32];
+                tmem_ld32(s_tmem, x);
+                const bool whole = __all_sync(0xffffffffu, n0 + kTile <= min_lim && sc[lane & 7].w != 0.f);
                 // Rare: a tile with hidden tokens (their products become -inf where they lie), or
                 // rows that have seen no token yet (their reference is set from this tile).
                 const bool start = __any_sync(0xffffffffu, m == kNoMax && p.valid);
@@ -561,6 +560,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
                     float best = -INFINITY;
 #pragma unroll 1
                     for (int c = 0; c < 4; ++c) {
+                        tmem_wait_ld();
                         tmem_ld32(s_tmem + 32 * c, x);
                         tmem_wait_ld();
                         float t[2] = {-INFINITY, -INFINITY};
@@ -579,6 +579,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
                     }
                     tmem_wait_st();
                     if (m == kNoMax && best != -INFINITY) m = best - kFresh;
+                    tmem_ld32(s_tmem, x);
                 }
                 // The row's 128 products, 32 at a time: exponents against the reference as it is,
                 // the next products on their way, weights, their sums by page group. No pass for
@@ -622,13 +623,21 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
                         if (lane == 0) mbar_arrive(p_full + 8 * (g * kPub + c / (4 / kPub)));
                     }
                 };
+                // The scores may be overwritten once every warp has read its last ones.
+                auto scores_read = [&]() {
+                    if (SEP) {
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(s_free + 8 * g);
+                    }
+                };
                 int from = 4;                                   // products that the slow loop takes
-                tmem_ld32(s_tmem, x);
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
                     tmem_wait_ld();
                     exponents(c);
                     if (c < 3) tmem_ld32(s_tmem + 32 * (c + 1), x);
+                    else scores_read();
                     weights();
                     // (w's own columns are free once the products of the unit before are done)
                     if (SEP && c == 0 && has) ok = wwait(o_done + 8 * g, (uint32_t)(units - 1) & 1);
@@ -643,9 +652,12 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
 #pragma unroll 1
                     for (int c = from; c < 4; ++c) {
                         tmem_wait_ld();
-                        tmem_ld32(s_tmem + 32 * c, x);
-                        tmem_wait_ld();
-                        exponents(c);
+                        if (c > from) {
+                            tmem_ld32(s_tmem + 32 * c, x);
+                            tmem_wait_ld();
+                            exponents(c);
+                            if (c == 3) scores_read();
+                        }
                         float top = u[0];
 #pragma unroll
                         for (int i = 1; i < 32; ++i) top = fmaxf(top, u[i]);
@@ -691,11 +703,6 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
                         place(c);
                     }
                     if (!ok) break;
-                }
-                if (SEP) {
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(s_free + 8 * g);          // the scores may be overwritten
                 }
                 has = true;
                 ++units;
