@@ -410,55 +410,63 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
                 if (!(ok = wwait(q_read, (pieces - 1) & 1))) break;
                 if (!(ok = wwait(s_full + 8 * ((q - 1) & 1), (uint32_t)((q - 1) >> 1) & 1))) break;
             }
-            // D / 8 lanes take a row, 8 channels each; eight rows of a lane are loaded at once
-            constexpr int LR = D / 8, RW = 32 / LR;              // lanes a row, rows a warp and load
+            // D / 8 lanes take a row, 8 channels each. The rows' bf16 channels are copied to
+            // where their two parts will be (as many bytes), all in flight at once; then each
+            // row is read, split and written back in place. (Little code: a piece's first
+            // instructions come from far.)
+            constexpr int LR = D / 8, RW = 32 / LR;              // lanes a row, rows a warp and step
             const int rl = lane / LR, c = lane % LR;
+            const int r_begin = (warp - 4) * (C::ROWS / 4), r_end = r_begin + C::ROWS / 4;
+            // raw channels 8 c .. of row r: the first half of a row in its e4m3 part's place
+            auto raw_at = [&](int r) {
+                return sbase + C::Q_OFF + (r >> 7) * 2 * C::TILE8 + (r & 127) * D + (c >= LR / 2 ? C::TILE8 + (c - LR / 2) * 16 : c * 16);
+            };
 #pragma unroll 1
-            for (int r0 = (warp - 4) * (C::ROWS / 4); r0 < (warp - 3) * (C::ROWS / 4); r0 += 8 * RW) {
-                uint4 v[8];
+            for (int r0 = r_begin; r0 < r_end; r0 += RW) {
+                const RowPlace p = row_place(a, pc.cur.s, pc.cur.b, pc.cur.rt, pc.cur.h, r0 + rl);
+                const __nv_bfloat16 *src = reinterpret_cast<const __nv_bfloat16 *>(a.Q) + p.q + 8 * c;
+                if ((reinterpret_cast<uintptr_t>(src) & 15) == 0 && p.valid) {
+                    cp_async16(raw_at(r0 + rl), src);
+                } else {
+                    uint32_t x[4] = {0, 0, 0, 0};
+                    const uint16_t *s = reinterpret_cast<const uint16_t *>(src);
+                    if (p.valid)
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const RowPlace p = row_place(a, pc.cur.s, pc.cur.b, pc.cur.rt, pc.cur.h, r0 + i * RW + rl);
-                    const __nv_bfloat16 *src = reinterpret_cast<const __nv_bfloat16 *>(a.Q) + p.q + 8 * c;
-                    v[i] = make_uint4(0, 0, 0, 0);
-                    if (p.valid) {
-                        if ((reinterpret_cast<uintptr_t>(src) & 15) == 0) {
-                            v[i] = *reinterpret_cast<const uint4 *>(src);
-                        } else {
-                            const uint16_t *s = reinterpret_cast<const uint16_t *>(src);
-                            v[i] = make_uint4(s[0] | (uint32_t)s[1] << 16, s[2] | (uint32_t)s[3] << 16,
-                                              s[4] | (uint32_t)s[5] << 16, s[6] | (uint32_t)s[7] << 16);
-                        }
-                    }
+                        for (int i = 0; i < 4; ++i) x[i] = s[2 * i] | (uint32_t)s[2 * i + 1] << 16;
+                    sts16(raw_at(r0 + rl), make_uint4(x[0], x[1], x[2], x[3]));
                 }
+            }
+            cp_async_commit();
+            cp_async_wait0();
+#pragma unroll 2
+            for (int r0 = r_begin; r0 < r_end; r0 += RW) {
+                const int r = r0 + rl, g = r >> 7, rg = r & 127;
+                const uint4 v = lds16(raw_at(r));                // (each lane reads what it copied)
+                const uint32_t x[4] = {v.x, v.y, v.z, v.w};
+                uint32_t top = 0;
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const int r = r0 + i * RW + rl, g = r >> 7, rg = r & 127;
-                    const uint32_t x[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-                    uint32_t top = 0;
+                for (int y = 0; y < 4; ++y) top = max(top, max(x[y] & 0x7fff0000u, (x[y] & 0x7fffu) << 16));
 #pragma unroll
-                    for (int y = 0; y < 4; ++y) top = max(top, max(x[y] & 0x7fff0000u, (x[y] & 0x7fffu) << 16));
+                for (int y = LR / 2; y; y >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, y));
+                const int e = imax((int)(top >> 23) - 127, -100);
+                const float inv = __int_as_float((7 - e + 127) << 23);
+                // (positive, so that -inf stays -inf; 1e-30 is as good as 0)
+                if (c == 0)
+                    factor[r] = top >= 0x7f800000u ? NAN : fmaxf(__int_as_float((e - 7 + 127) << 23) * a.sl2, 1e-30f);
+                uint32_t hi[4], lo[4];
 #pragma unroll
-                    for (int y = LR / 2; y; y >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, y));
-                    const int e = imax((int)(top >> 23) - 127, -100);
-                    const float inv = __int_as_float((7 - e + 127) << 23);
-                    // (positive, so that -inf stays -inf; 1e-30 is as good as 0)
-                    if (c == 0)
-                        factor[r] = top >= 0x7f800000u ? NAN : fmaxf(__int_as_float((e - 7 + 127) << 23) * a.sl2, 1e-30f);
-                    uint32_t hi[4], lo[4];
-#pragma unroll
-                    for (int y = 0; y < 4; ++y) {
-                        const float f0 = __uint_as_float(x[y] << 16) * inv, f1 = __uint_as_float(x[y] & 0xffff0000u) * inv;
-                        hi[y] = pack_e4m3(f0, f1);
-                        const float2 kept = float2_of(f16x2_of_e4m3x2(hi[y]));
-                        lo[y] = pack_e5m2(f0 - kept.x, f1 - kept.y);
-                    }
-                    const int ch = c >> 1;                        // 16-byte chunk of the row of codes
-                    const uint32_t at = sbase + C::Q_OFF + g * 2 * C::TILE8 + rg * D +
-                                        (D == 128 ? ch ^ (rg & 7) : ch ^ ((rg >> 1) & 3)) * 16 + 8 * (c & 1);
-                    asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(at), "r"(hi[0] | hi[1] << 16), "r"(hi[2] | hi[3] << 16) : "memory");
-                    asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(at + C::TILE8), "r"(lo[0] | lo[1] << 16), "r"(lo[2] | lo[3] << 16) : "memory");
+                for (int y = 0; y < 4; ++y) {
+                    const float f0 = __uint_as_float(x[y] << 16) * inv, f1 = __uint_as_float(x[y] & 0xffff0000u) * inv;
+                    hi[y] = pack_e4m3(f0, f1);
+                    const float2 kept = float2_of(f16x2_of_e4m3x2(hi[y]));
+                    lo[y] = pack_e5m2(f0 - kept.x, f1 - kept.y);
                 }
+                __syncwarp();                                    // the whole row has been read
+                const int ch = c >> 1;                           // 16-byte chunk of the row of codes
+                const uint32_t at = sbase + C::Q_OFF + g * 2 * C::TILE8 + rg * D +
+                                    (D == 128 ? ch ^ (rg & 7) : ch ^ ((rg >> 1) & 3)) * 16 + 8 * (c & 1);
+                asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(at), "r"(hi[0] | hi[1] << 16), "r"(hi[2] | hi[3] << 16) : "memory");
+                asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(at + C::TILE8), "r"(lo[0] | lo[1] << 16), "r"(lo[2] | lo[3] << 16) : "memory");
             }
             fence_proxy_async_smem();
             __syncwarp();
@@ -557,25 +565,21 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
                 // rows that have seen no token yet (their reference is set from this tile).
                 const bool start = __any_sync(0xffffffffu, m == kNoMax && p.valid);
                 if (__builtin_expect(start || !whole, 0)) {
+                    // (eight at a time: little code, which comes from far when it is run once an item)
                     float best = -INFINITY;
+                    tmem_wait_ld();
 #pragma unroll 1
-                    for (int c = 0; c < 4; ++c) {
+                    for (int c = 0; c < kTile; c += 8) {
+                        uint32_t y[8];
+                        tmem_ld8(s_tmem + c, y);
+                        const float4 f = sc[c >> 4];
                         tmem_wait_ld();
-                        tmem_ld32(s_tmem + 32 * c, x);
-                        tmem_wait_ld();
-                        float t[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) {
-                            if (n0 + 32 * c + i >= lim || sc[2 * c + (i >> 4)].w == 0.f) x[i] = 0xff800000u;
-                            t[i >> 4] = fmaxf(t[i >> 4], __uint_as_float(x[i]));
+                        for (int i = 0; i < 8; ++i) {
+                            if (n0 + c + i >= lim || f.w == 0.f) y[i] = 0xff800000u;
+                            best = fmaxf(best, fmaf(__uint_as_float(y[i]), fac * f.x, f.y));
                         }
-                        if (!whole) tmem_st32(s_tmem + 32 * c, x);
-                        // (the factors are positive: a page group's largest product is its largest score)
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            const float4 f = sc[2 * c + h];
-                            best = fmaxf(best, fmaf(t[h], fac * f.x, f.y));
-                        }
+                        tmem_st8(s_tmem + c, y);
                     }
                     tmem_wait_st();
                     if (m == kNoMax && best != -INFINITY) m = best - kFresh;

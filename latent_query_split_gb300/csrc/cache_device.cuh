@@ -154,7 +154,7 @@ struct RowPlace {
     int limit;                           // tokens it sees
     int64_t q, o, l;                     // element offsets
 };
-static __device__ __noinline__ RowPlace row_place(const AttnArgs &a, const Seq &s, int b, int rt, int h, int row) {
+__device__ __forceinline__ RowPlace row_place(const AttnArgs &a, const Seq &s, int b, int rt, int h, int row) {
     RowPlace p;
     const unsigned rr = (unsigned)rt * a.rows + row;            // rows of a head: under 2^31
     p.valid = rr < (unsigned)(s.n * a.G);
