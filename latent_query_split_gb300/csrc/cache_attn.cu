@@ -171,51 +171,86 @@ __global__ void __launch_bounds__(128) attn_simt_kernel(const __grid_constant__ 
 }
 
 // ---- merge --------------------------------------------------------------------------
-// One warp a row of the item that ends in span blockIdx.x: its pieces lie in
-// spans first .. blockIdx.x, the first in slot 1 (it began there) and the rest
-// in slot 0. They are added in that order, so results do not vary. A piece
-// without a visible token has l = 0. Bound by latency: a few KB a row.
+// The item that ends in span blockIdx.x: its pieces lie in spans first ..
+// blockIdx.x, the first in slot 1 (it began there) and the rest in slot 0. They are
+// added in a fixed order, so results do not vary. A piece without a visible token
+// has l = 0. Bound by latency: a few KB a row, in two rounds of loads.
+//   ROW: one block a row, its warps share the pieces (few rows of many pieces);
+//   else one warp a row (many rows of few pieces).
+template <bool ROW>
 __global__ void __launch_bounds__(128) attn_merge_kernel(const __grid_constant__ AttnArgs a, const int f32) {
+    __shared__ float f_sh[ROW ? kMaxSpans : 1], red[8];
+    __shared__ float4 o_sh[ROW ? 3 : 1][32];
     tc::pdl_wait();
     const int4 rec = a.rec[blockIdx.x];
     if (rec.x < 0) return;
-    const int lane = threadIdx.x & 31, r = blockIdx.y * 4 + (threadIdx.x >> 5);
+    const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
+    const int r = ROW ? (int)blockIdx.y : (int)blockIdx.y * 4 + w;
     const int D = a.c.D, first = rec.w, count = (int)blockIdx.x - first + 1;
     if (r >= a.rows) return;
     const Seq s = load_seq(a, rec.x);
     const RowPlace p = row_place(a, s, rec.x, rec.y, rec.z, r);
     if (!p.valid) return;
-    auto slot = [&](int i) { return ((int64_t)(first + i) * 2 + (i == 0 ? 1 : 0)) * a.rows + r; };
+    const int64_t step = 2 * (int64_t)a.rows, base = (int64_t)first * step + r;
+    auto slot = [&](int i) { return base + i * step + (i == 0 ? a.rows : 0); };
+    // weights of the pieces; this thread's are i0, i0 + NT, ...
+    constexpr int NT = ROW ? 128 : 32;
+    const int i0 = ROW ? tid : lane;
     float M = -INFINITY;
-    for (int i = lane; i < count; i += 32) {
+    for (int i = i0; i < count; i += NT) {
         const float2 ml = a.part_ml[slot(i)];
         if (!(ml.y == 0.f)) M = fmaxf(M, ml.x);
     }
 #pragma unroll
     for (int x = 16; x; x >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, x));
+    if (ROW) {
+        if (lane == 0) red[w] = M;
+        __syncthreads();
+        M = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
+    }
     const float ref = M == -INFINITY ? 0.f : M;
     float l = 0.f;
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int base = 0; base < count; base += 32) {
-        float f = 0.f;
-        if (base + lane < count) {
-            const float2 ml = a.part_ml[slot(base + lane)];
-            f = ml.y == 0.f ? 0.f : tc::ex2(ml.x - ref);
-            l += f * ml.y;
+    auto add = [&](float g, int i) {
+        if (4 * lane < D) {
+            const float4 y = *reinterpret_cast<const float4 *>(&a.part_O[slot(i) * D + 4 * lane]);
+            v.x = fmaf(g, y.x, v.x); v.y = fmaf(g, y.y, v.y);
+            v.z = fmaf(g, y.z, v.z); v.w = fmaf(g, y.w, v.w);
         }
-        const int m = imin(32, count - base);
+    };
+    auto weight = [&](int i) {
+        const float2 ml = a.part_ml[slot(i)];
+        const float f = ml.y == 0.f ? 0.f : tc::ex2(ml.x - ref);
+        l += f * ml.y;
+        return f;
+    };
+    if (ROW) {
+        for (int i = i0; i < count; i += NT) f_sh[i] = weight(i);
+        __syncthreads();
+#pragma unroll 8
+        for (int i = w; i < count; i += 4) add(f_sh[i], i);
+    } else {
+        for (int b = 0; b < count; b += 32) {
+            const float f = b + lane < count ? weight(b + lane) : 0.f;
+            const int m = imin(32, count - b);
 #pragma unroll 4
-        for (int i = 0; i < m; ++i) {
-            const float g = __shfl_sync(0xffffffffu, f, i);
-            if (4 * lane < D) {
-                const float4 y = *reinterpret_cast<const float4 *>(&a.part_O[slot(base + i) * D + 4 * lane]);
-                v.x = fmaf(g, y.x, v.x); v.y = fmaf(g, y.y, v.y);
-                v.z = fmaf(g, y.z, v.z); v.w = fmaf(g, y.w, v.w);
-            }
+            for (int i = 0; i < m; ++i) add(__shfl_sync(0xffffffffu, f, i), b + i);
         }
     }
 #pragma unroll
     for (int x = 16; x; x >>= 1) l += __shfl_xor_sync(0xffffffffu, l, x);
+    if (ROW) {
+        if (lane == 0) red[4 + w] = l;
+        if (w > 0) o_sh[w - 1][lane] = v;
+        __syncthreads();
+        if (w > 0) return;
+        l = (red[4] + red[5]) + (red[6] + red[7]);
+#pragma unroll
+        for (int x = 0; x < 3; ++x) {
+            const float4 y = o_sh[x][lane];
+            v.x += y.x; v.y += y.y; v.z += y.z; v.w += y.w;
+        }
+    }
     const float inv = l == 0.f ? 0.f : 1.f / l;
     if (4 * lane < D)
         store_o4(a, f32 != 0, p.o + 4 * lane, make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv));
@@ -245,7 +280,7 @@ AttnPlan attn_plan(const Pool &c, int G, bool bf16, int64_t T, bool ragged, int 
     const int64_t tiles = ((T * G + p.rows - 1) / p.rows + c.B) * c.H *
                           (((int64_t)c.W * c.page + kTile - 1) / kTile + 1);
     if (grid > tiles) grid = tiles;
-    p.grid = (int)(grid < 1 ? 1 : grid);
+    p.grid = (int)(grid < 1 ? 1 : grid > kMaxSpans ? kMaxSpans : grid);
     auto up = [](size_t x) { return (x + 255) & ~(size_t)255; };
     size_t o = up(sizeof(float) * 2 * p.grid * p.rows * c.D);
     p.part_ml = o;
@@ -288,8 +323,9 @@ cudaError_t launch_attn(const AttnArgs &a, const AttnPlan &plan, bool bf16, cuda
         e = launch_attn_mma(a, bf16, plan.cluster, st);
     }
     if (e != cudaSuccess || plan.cluster > 1) return e;
-    e = launch_pdl(attn_merge_kernel, dim3(a.grid, (a.rows + 3) / 4), dim3(128), st, a,
-                   (int)(!bf16 || a.o_f32));
+    const int f32 = !bf16 || a.o_f32;
+    e = a.rows <= 32 ? launch_pdl(attn_merge_kernel<true>, dim3(a.grid, a.rows), dim3(128), st, a, f32)
+                     : launch_pdl(attn_merge_kernel<false>, dim3(a.grid, a.rows / 4), dim3(128), st, a, f32);
     if (e != cudaSuccess) return e;
     note_launch();
     return cudaGetLastError();

@@ -16,6 +16,7 @@ namespace flare {
 namespace cache {
 
 constexpr int kTile = 128;       // tokens of one tile of the attention's work
+constexpr int kMaxSpans = 1024;  // spans of a call at most
 
 FLARE_HD int imin(int a, int b) { return a < b ? a : b; }
 FLARE_HD int imax(int a, int b) { return a > b ? a : b; }
