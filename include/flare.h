@@ -422,7 +422,9 @@ FLARE_API size_t flare_cache_workspace_bytes(const flare_cache_dims_t *dims, int
  * what they hold. A token on a page number outside the pool is not seen, and
  * the device status is set. Softmax and sums are fp32; the kernels for bf16
  * round the weights exp(S - max) to fp16 where they meet the values.
- * workspace: flare_cache_workspace_bytes(dims, T) bytes, 256-byte aligned.
+ * workspace: flare_cache_workspace_bytes(dims, T) bytes, 256-byte aligned
+ * (equal sequences of few rows over few tokens need none: such a call succeeds
+ * with NULL, where others return FLARE_ERR_WORKSPACE).
  */
 FLARE_API flare_status_t flare_cache_attn(const flare_cache_dims_t *dims, const flare_cache_t *cache,
                                           const void *Q, int64_t q_stride, int64_t T,

@@ -111,7 +111,7 @@ flare_status_t attn_run(const flare_cache_dims_t *d, const flare_cache_t *cache,
     if (!aligned(Q, es) || !aligned(O, o_f32 ? 4 : es) || !aligned(L, 4))
         return fail(FLARE_ERR_INVALID_ARG, "tensors must be aligned to their element size");
     const AttnPlan plan = plan_for(d, G, T, cu != nullptr);
-    if (!ws || ws_bytes < plan.bytes)
+    if (plan.cluster == 1 && (!ws || ws_bytes < plan.bytes))
         return fail(FLARE_ERR_WORKSPACE, "workspace of %zu bytes required, %zu given", plan.bytes, ws_bytes);
     if (!aligned(ws, 256)) return fail(FLARE_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
     if (check_only) return FLARE_OK;

@@ -447,24 +447,24 @@ _F8, _F32, _I32 = torch.float8_e4m3fn, torch.float32, torch.int32
 def _cache_args(cache: FlareCache):
     """(packed pointers, device, (B, W), (P, H, page, D)) of a cache after checks."""
     k, v, ks, vs, table = cache
-    shape, scales, dev = k.shape, ks.shape, k.device
-    if k.dtype != _F8 or v.dtype != _F8:
+    shape, scales, rows, dev = k.shape, ks.shape, table.shape, k.get_device()
+    if k.dtype is not _F8 or v.dtype is not _F8:
         raise TypeError("a cache's codes are float8_e4m3fn")
-    if ks.dtype != _F32 or vs.dtype != _F32 or table.dtype != _I32:
+    if ks.dtype is not _F32 or vs.dtype is not _F32 or table.dtype is not _I32:
         raise TypeError("a cache's scales are float32 and its page table is int32")
-    if len(shape) != 4 or table.dim() != 2 or v.shape != shape or scales != shape[:2] or vs.shape != scales:
+    if len(shape) != 4 or len(rows) != 2 or v.shape != shape or scales != shape[:2] or vs.shape != scales:
         raise ValueError("cache shapes do not match: k, v [P, H, page, D], scales [P, H], page_table [B, W]")
-    if dev.type != "cuda":
+    if dev < 0:
         raise ValueError("device tensor expected")
-    if v.device != dev or ks.device != dev or vs.device != dev or table.device != dev:
+    if not (v.get_device() == ks.get_device() == vs.get_device() == table.get_device() == dev):
         raise ValueError("the cache's tensors are on different devices")
-    if dev.index != torch.cuda.current_device():
+    if dev != torch.cuda.current_device():
         raise ValueError("the cache is not on the current device")
     if not (k.is_contiguous() and v.is_contiguous() and ks.is_contiguous() and vs.is_contiguous() and
             table.is_contiguous()):
         raise ValueError("contiguous tensor expected")
-    return (_PACK_PTRS(k.data_ptr(), v.data_ptr(), ks.data_ptr(), vs.data_ptr(), table.data_ptr()), dev,
-            table.shape, shape)
+    return (_PACK_PTRS(k.data_ptr(), v.data_ptr(), ks.data_ptr(), vs.data_ptr(), table.data_ptr()), k.device,
+            rows, shape)
 
 
 def _cache_dims(rows, shape, Hq: int, dtype, scale=None, kernel="auto"):
@@ -486,32 +486,27 @@ def _like(t, what, dtype, shape, device):
     """Pointer of an optional tensor after checks of its type, shape and device."""
     if t is None:
         return None
-    if t.dtype != dtype or t.shape != shape:
+    if t.dtype is not dtype or t.shape != shape:
         raise ValueError(f"{what} must be {dtype} of shape {tuple(shape)}")
-    if t.device != device:
+    if t.get_device() != device.index:
         raise ValueError(f"{what} is on another device than the cache")
     if not t.is_contiguous():
         raise ValueError(f"{what} must be contiguous")
     return t.data_ptr()
 
 
-def _on_stream(call):
-    """A cache call with `stream` given runs with that stream current: what it
+def _on(stream, call, *args, **kw):
+    """A cache call that is given a stream runs with that stream current: what it
     allocates is then ordered with its kernels, not with another stream's."""
-    @functools.wraps(call)
-    def on(*args, stream=None, **kw):
-        if stream is None:
-            return call(*args, **kw)
-        with torch.cuda.stream(stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream))):
-            return call(*args, **kw)
-    return on
+    with torch.cuda.stream(stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream))):
+        return call(*args, **kw)
 
 
 def _rows(x, what, heads, D, B, cu, dtype, device):
     """(pointer, token stride, T) of token rows [B, n, heads, D] or, with
     cu_seqlens, [T, heads, D]; a token's channels are contiguous, the tokens
     evenly spaced."""
-    if x.dtype != dtype:
+    if x.dtype is not dtype:
         raise TypeError(f"{what} must be {dtype}")
     shape = x.shape
     if len(shape) != (4 if cu is None else 3) or shape[-2] != heads or shape[-1] != D or (cu is None and shape[0] != B):
@@ -531,13 +526,15 @@ def _rows(x, what, heads, D, B, cu, dtype, device):
     return x.data_ptr(), (step if T > 1 else 0), T
 
 
-@_on_stream
 def flare_cache_append(cache: FlareCache, K, V, seq_lens, *, cu_seqlens=None, Q=None, inv_freq=None,
-                       interleaved=False, Q_out=None, seq_lens_out=None):
+                       interleaved=False, Q_out=None, seq_lens_out=None, stream=None):
     """New tokens K, V ([B,n,H,D], or [T,H,D] with int32 cu_seqlens [B+1]) enter
     the cache behind the seq_lens tokens that each sequence holds; with inv_freq
     (fp32 [rot/2]) keys and the queries Q are rotated by their positions.
     Returns (seq_lens_out, Q_out)."""
+    if stream is not None:
+        return _on(stream, flare_cache_append, cache, K, V, seq_lens, cu_seqlens=cu_seqlens, Q=Q, inv_freq=inv_freq,
+                   interleaved=interleaved, Q_out=Q_out, seq_lens_out=seq_lens_out)
     lib = _lib or load_library()
     ptrs, dev, table, shape = _cache_args(cache)
     (B, _), (_, H, _, D), dtype = table, shape, K.dtype
@@ -595,12 +592,14 @@ def _cache_workspace(dims, T, workspace, device):
     return workspace, _ptr(workspace), workspace.numel() * workspace.element_size()
 
 
-@_on_stream
 def flare_cache_attn(Q, cache: FlareCache, seq_lens, *, cu_seqlens=None, causal=True, O=None, L=None,
-                     workspace=None, scale=None, kernel="auto"):
+                     workspace=None, scale=None, kernel="auto", stream=None):
     """Attention of Q ([B,n,Hq,D], or [T,Hq,D] with int32 cu_seqlens [B+1]) over
     the seq_lens tokens that the cache holds for each sequence; returns (O, L):
     O like Q, L fp32 without the channels."""
+    if stream is not None:
+        return _on(stream, flare_cache_attn, Q, cache, seq_lens, cu_seqlens=cu_seqlens, causal=causal, O=O, L=L,
+                   workspace=workspace, scale=scale, kernel=kernel)
     lib = _lib or load_library()
     ptrs, dev, table, shape = _cache_args(cache)
     B, dtype, rows = table[0], Q.dtype, Q.shape
@@ -617,11 +616,16 @@ def flare_cache_attn(Q, cache: FlareCache, seq_lens, *, cu_seqlens=None, causal=
         l = L.data_ptr()
     else:
         l = _like(L, "L", _F32, rows[:-1], dev)
-    workspace, ws, nbytes = _cache_workspace(dims, T, workspace, dev)
-    status = lib.flare_cache_attn(
-        dims, ptrs, q, q_st, T, _like(seq_lens, "seq_lens", _I32, (B,), dev),
-        _like(cu_seqlens, "cu_seqlens", _I32, (B + 1,), dev), int(causal), o, l, ws, nbytes,
-        _raw_stream(dev.index))
+    lens, cu = _like(seq_lens, "seq_lens", _I32, (B,), dev), _like(cu_seqlens, "cu_seqlens", _I32, (B + 1,), dev)
+    ws = nbytes = None
+    if workspace is not None:
+        workspace, ws, nbytes = _cache_workspace(dims, T, workspace, dev)
+    status = lib.flare_cache_attn(dims, ptrs, q, q_st, T, lens, cu, int(causal), o, l, ws, nbytes or 0,
+                                  _raw_stream(dev.index))
+    if status == FLARE_ERR_WORKSPACE and workspace is None:          # (small calls need none)
+        workspace, ws, nbytes = _cache_workspace(dims, T, None, dev)
+        status = lib.flare_cache_attn(dims, ptrs, q, q_st, T, lens, cu, int(causal), o, l, ws, nbytes,
+                                      _raw_stream(dev.index))
     if status:
         _check(status)
     return O, L
@@ -636,11 +640,13 @@ def _latents(Q, B, shape, device):
     return _ptr(Q), M, (0 if Q.dim() == 3 else H * M * D)
 
 
-@_on_stream
 def flare_cache_encoder_fwd(Q, cache: FlareCache, seq_lens, *, Z=None, L=None, workspace=None, scale=None,
-                            kernel="auto"):
+                            kernel="auto", stream=None):
     """The FLARE encoder over the cached tokens: latent queries Q ([H,M,D] or
     [B,H,M,D]); returns (Z [B,H,M,D], L [B,H,M]) in fp32."""
+    if stream is not None:
+        return _on(stream, flare_cache_encoder_fwd, Q, cache, seq_lens, Z=Z, L=L, workspace=workspace,
+                   scale=scale, kernel=kernel)
     lib = _lib or load_library()
     ptrs, dev, table, shape = _cache_args(cache)
     (B, _), (_, H, _, D) = table, shape
@@ -657,12 +663,14 @@ def flare_cache_encoder_fwd(Q, cache: FlareCache, seq_lens, *, Z=None, L=None, w
     return Z, L
 
 
-@_on_stream
 def flare_cache_fwd(Q, cache: FlareCache, K, V, seq_lens, *, seq_lens_out=None, Y=None, Z=None, L=None,
-                    workspace=None, scale=None, kernel="auto"):
+                    workspace=None, scale=None, kernel="auto", stream=None):
     """FLARE mixer forward over a growing token set: K, V [B,N,H,D] enter the
     cache, the latents Q gather Z from all the tokens held, the new tokens decode
     against them; returns (Y [B,N,H,D], Z, L, seq_lens_out)."""
+    if stream is not None:
+        return _on(stream, flare_cache_fwd, Q, cache, K, V, seq_lens, seq_lens_out=seq_lens_out, Y=Y, Z=Z, L=L,
+                   workspace=workspace, scale=scale, kernel=kernel)
     lib = _lib or load_library()
     ptrs, dev, table, shape = _cache_args(cache)
     (B, _), (_, H, _, D) = table, shape

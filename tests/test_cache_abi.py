@@ -94,7 +94,8 @@ def test_attn_refuses(lib, kw):
 def test_attn_needs_its_workspace_and_query_heads(lib):
     need = lib.flare_cache_workspace_bytes(bytes(_dims()), 4)
     assert need > 0
-    assert _attn(lib, _dims(), wsb=need - 1) == WORKSPACE and _attn(lib, _dims(), ws=None) == WORKSPACE
+    assert _attn(lib, _dims(), cu=A[12], wsb=need - 1) == WORKSPACE and _attn(lib, _dims(), cu=A[12], ws=None) == WORKSPACE
+    assert _attn(lib, _dims(), T=400, ws=None) == WORKSPACE and _attn(lib, _dims(W=8192), ws=None) == WORKSPACE
     assert _attn(lib, _dims(Hq=0)) == INVALID
     assert _append(lib, _dims(Hq=0)) == INVALID
     assert _append(lib, _dims(H=4, Hq=0), Q=A[8], Qo=A[9]) == INVALID
@@ -113,7 +114,7 @@ def test_mixer_checks_every_stage_before_launching(lib):
     for kw in (dict(M=0), dict(N=-1), dict(Q=None), dict(qbs=5), dict(K=None), dict(V=None), dict(lens=None), dict(out=None),
                dict(out=A[8]), dict(Y=None), dict(Z=None), dict(L=None), dict(ws=1 + (1 << 40))):
         assert call(**kw) == INVALID, kw
-    assert call(wsb=0) == WORKSPACE
+    assert call(wsb=0, M=128) == WORKSPACE
     assert call(M=300) == UNSUPPORTED              # the decode's latents
 
 

@@ -685,6 +685,25 @@ def test_two_streams_at_once():
             assert torch.equal(O, want[s][0]) and torch.equal(L, want[s][1])
 
 
+def test_given_stream():
+    """Calls with `stream` run there, and what they allocate belongs to it."""
+    H, G, D, page = 2, 4, 64, 32
+    cache = make_cache(1, 40, H, D, page)
+    fill(cache, [600], seed=47)
+    g = torch.Generator().manual_seed(48)
+    K, V, Q = (torch.randn((1, 40, h, D), generator=g).bfloat16().cuda() for h in (H, H, H * G))
+    side, lens = torch.cuda.Stream(), ints([600])
+    side.wait_stream(torch.cuda.current_stream())
+    before = cache_ref.host(cache)
+    for stream in (side, side.cuda_stream):
+        out, q = flare.flare_cache_append(cache, K, V, lens, Q=Q, inv_freq=freqs(D), stream=stream)
+        O, L = flare.flare_cache_attn(q, cache, out, stream=stream)
+        Z, _ = flare.flare_cache_encoder_fwd(Q[0].transpose(0, 1)[:H].contiguous(), cache, out, stream=stream)
+    side.synchronize()
+    check_append(cache, before, K[0], V[0], Q[0], [600], [40], freqs(D), False, out, q[0])
+    check_attn(O[0], L[0], q[0], cache, [640], [40], True)
+
+
 # ---- the FLARE encoder and mixer over the cache ------------------------------------------
 @pytest.mark.parametrize("dtype,M,D,per_batch", [("bf16", 64, 64, False), ("bf16", 128, 128, True), ("bf16", 256, 64, False),
                                                  ("bf16", 20, 32, True), ("fp32", 16, 32, False), ("fp32", 33, 64, True)])
