@@ -275,10 +275,14 @@ __device__ __forceinline__ uint32_t finite_top(const Raw<BF16> &r, bool &bad) {
 // are computed once for the block's heads. Queries have no scale: they stream.
 // Bound by memory: each token is read once and written once. One pass with the
 // tile in registers reads half of what a pass for the scale and one for the codes
-// would. 24,213 tokens with 8 cache and 32 query heads of 128 (529 MB): see the
-// launcher.
+// would. 24,213 bfloat16 tokens with 8 cache and 32 query heads of 128 (529 MB):
+// 117 us, 4.5 TB/s. What is left is the page's own turnaround: load, join the
+// maxima, round, store, with two to three blocks of 256 threads a multiprocessor to
+// cover it; three at TPT = 1 (80 registers) take 1,000 float32 tokens with 4 and 8
+// heads of 96 from 36.8 to 32.5 us, four 33.4, and one more register cut at TPT = 2
+// spills (117 to 122 us).
 template <bool BF16, bool INTER, int TPT>
-__global__ void __launch_bounds__(256) append_page_kernel(const AppendArgs a, const int thr, const int kv_parts,
+__global__ void __launch_bounds__(256, TPT == 1 ? 3 : TPT == 2 ? 2 : 1) append_page_kernel(const AppendArgs a, const int thr, const int kv_parts,
                                                           const int kv_heads, const int q_heads) {
     __shared__ Slot sl;
     __shared__ uint64_t freq[64];
