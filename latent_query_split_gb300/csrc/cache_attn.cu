@@ -20,16 +20,14 @@ namespace cache {
 template <int R, bool BF16>
 __global__ void __launch_bounds__(128) attn_simt_kernel(const __grid_constant__ AttnArgs a) {
     constexpr int NT = 128, NW = 4;
-    __shared__ int64_t scan_sh[NW];
-    __shared__ Cursor cur_sh;
     __shared__ __align__(16) float q_sh[R][128];
     __shared__ __align__(16) float p_sh[NW][R][32];
     __shared__ __align__(16) float o_sh[NW][R][128];
     __shared__ float m_sh[NW][R], l_sh[NW][R];
     const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5, cta = blockIdx.x;
     const int D = a.c.D;
-    const Span sp = find_span<NT>(a, cta, scan_sh, &cur_sh);
-    Cursor cur = cur_sh;
+    Cursor cur;
+    const Span sp = find_spans<NT, 1, kTile>(a, cur);
     if (tid == 0) write_record(a, sp, cur, cta);
     while (cur.tiles_left > 0) {
         const int k0 = cur.k, k1 = imin(cur.nt, cur.k + cur.tiles_left);
@@ -165,96 +163,134 @@ __global__ void __launch_bounds__(128) attn_simt_kernel(const __grid_constant__ 
             }
         }
         cur.tiles_left -= k1 - k0;
-        if (cur.tiles_left > 0) next_item(a, cur);
+        if (cur.tiles_left > 0) next_item<kTile>(a, cur);
     }
     tc::pdl_launch_dependents();
 }
 
 // ---- merge --------------------------------------------------------------------------
-// The item that ends in span blockIdx.x: its pieces lie in spans first ..
-// blockIdx.x, the first in slot 1 (it began there) and the rest in slot 0. They are
-// added in a fixed order, so results do not vary. A piece without a visible token
-// has l = 0. Bound by latency: a few KB a row, in two rounds of loads.
-//   ROW: one block a row, its warps share the pieces (few rows of many pieces);
-//   else one warp a row (many rows of few pieces).
-template <bool ROW>
-__global__ void __launch_bounds__(128) attn_merge_kernel(const __grid_constant__ AttnArgs a, const int f32) {
-    __shared__ float f_sh[ROW ? kMaxSpans : 1], red[8];
-    __shared__ float4 o_sh[ROW ? 3 : 1][32];
+// An item that ends in span `last` but began in span `first`: its pieces lie in spans
+// first .. last, the first in slot 1 (it began there) and the rest in slot 0. They are
+// added in a fixed order, so results do not vary. A piece without a visible token has
+// l = 0. Bound by latency: a few KB a row, so a warp has the statistics and the outputs of
+// eight pieces on their way at once and joins them under a running reference.
+struct Merged {
+    float m, l;
+    float4 v;
+    __device__ __forceinline__ Merged() : m(-INFINITY), l(0.f), v(make_float4(0.f, 0.f, 0.f, 0.f)) {}
+    // N states more; those with l = 0 have no part
+    template <int N>
+    __device__ __forceinline__ void add(const float2 (&ml)[N], const float4 (&o)[N]) {
+        float top = m;
+#pragma unroll
+        for (int y = 0; y < N; ++y)
+            if (!(ml[y].y == 0.f)) top = fmaxf(top, ml[y].x);
+        const float ref = top == -INFINITY ? 0.f : top, f = m == -INFINITY ? 0.f : tc::ex2(m - ref);
+        m = top;
+        l *= f;
+        v.x *= f; v.y *= f; v.z *= f; v.w *= f;
+#pragma unroll
+        for (int y = 0; y < N; ++y) {
+            if (ml[y].y == 0.f) continue;
+            const float g = tc::ex2(ml[y].x - ref);
+            l = fmaf(g, ml[y].y, l);
+            v.x = fmaf(g, o[y].x, v.x); v.y = fmaf(g, o[y].y, v.y);
+            v.z = fmaf(g, o[y].z, v.z); v.w = fmaf(g, o[y].w, v.w);
+        }
+    }
+};
+// Pieces i, i + n, ... of row r of the item in spans first .. last; four channels a lane.
+template <int N>
+__device__ __forceinline__ Merged merge_pieces(const AttnArgs &a, int first, int last, int r, int i, int n) {
+    const int64_t base = (int64_t)first * 2 * a.rows + r;
+    const int D = a.c.D, count = last - first + 1, d = 4 * (threadIdx.x & 31);
+    Merged s;
+#pragma unroll 1
+    for (; i < count; i += N * n) {
+        float2 ml[N];
+        float4 o[N];
+#pragma unroll
+        for (int y = 0; y < N; ++y) {
+            const int x = i + y * n;
+            const int64_t slot = base + (int64_t)x * 2 * a.rows + (x == 0 ? a.rows : 0);
+            ml[y] = make_float2(0.f, 0.f);
+            o[y] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (x < count) {
+                ml[y] = a.part_ml[slot];
+                if (d < D) o[y] = *reinterpret_cast<const float4 *>(&a.part_O[slot * D + d]);
+            }
+        }
+        s.add(ml, o);
+    }
+    return s;
+}
+__device__ __forceinline__ void store_row(const AttnArgs &a, const RowPlace &p, bool f32, const Merged &s) {
+    const int d = 4 * (threadIdx.x & 31);
+    const float inv = s.l == 0.f ? 0.f : 1.f / s.l;
+    if (d < a.c.D) store_o4(a, f32, p.o + d, make_float4(s.v.x * inv, s.v.y * inv, s.v.z * inv, s.v.w * inv));
+    if (a.L && d == 0) a.L[p.l] = s.l == 0.f ? -INFINITY : (s.m + log2f(s.l)) * kLn2;
+}
+// Many rows, few spans: one warp a row of the item that ends in span blockIdx.x.
+__global__ void __launch_bounds__(128) attn_merge_rows_kernel(const __grid_constant__ AttnArgs a, const int f32) {
     tc::pdl_wait();
     const int4 rec = a.rec[blockIdx.x];
     if (rec.x < 0) return;
-    const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
-    const int r = ROW ? (int)blockIdx.y : (int)blockIdx.y * 4 + w;
-    const int D = a.c.D, first = rec.w, count = (int)blockIdx.x - first + 1;
-    if (r >= a.rows) return;
-    const Seq s = load_seq(a, rec.x);
-    const RowPlace p = row_place(a, s, rec.x, rec.y, rec.z, r);
-    if (!p.valid) return;
-    const int64_t step = 2 * (int64_t)a.rows, base = (int64_t)first * step + r;
-    auto slot = [&](int i) { return base + i * step + (i == 0 ? a.rows : 0); };
-    // weights of the pieces; this thread's are i0, i0 + NT, ...
-    constexpr int NT = ROW ? 128 : 32;
-    const int i0 = ROW ? tid : lane;
-    float M = -INFINITY;
-    for (int i = i0; i < count; i += NT) {
-        const float2 ml = a.part_ml[slot(i)];
-        if (!(ml.y == 0.f)) M = fmaxf(M, ml.x);
-    }
-#pragma unroll
-    for (int x = 16; x; x >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, x));
-    if (ROW) {
-        if (lane == 0) red[w] = M;
-        __syncthreads();
-        M = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
-    }
-    const float ref = M == -INFINITY ? 0.f : M;
-    float l = 0.f;
-    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-    auto add = [&](float g, int i) {
-        if (4 * lane < D) {
-            const float4 y = *reinterpret_cast<const float4 *>(&a.part_O[slot(i) * D + 4 * lane]);
-            v.x = fmaf(g, y.x, v.x); v.y = fmaf(g, y.y, v.y);
-            v.z = fmaf(g, y.z, v.z); v.w = fmaf(g, y.w, v.w);
-        }
-    };
-    auto weight = [&](int i) {
-        const float2 ml = a.part_ml[slot(i)];
-        const float f = ml.y == 0.f ? 0.f : tc::ex2(ml.x - ref);
-        l += f * ml.y;
-        return f;
-    };
-    if (ROW) {
-        for (int i = i0; i < count; i += NT) f_sh[i] = weight(i);
-        __syncthreads();
-#pragma unroll 8
-        for (int i = w; i < count; i += 4) add(f_sh[i], i);
-    } else {
-        for (int b = 0; b < count; b += 32) {
-            const float f = b + lane < count ? weight(b + lane) : 0.f;
-            const int m = imin(32, count - b);
-#pragma unroll 4
-            for (int i = 0; i < m; ++i) add(__shfl_sync(0xffffffffu, f, i), b + i);
+    const int r = (int)blockIdx.y * 4 + (int)(threadIdx.x >> 5);
+    const RowPlace p = row_place(a, load_seq(a, rec.x), rec.x, rec.y, rec.z, r);
+    if (p.valid) store_row(a, p, f32 != 0, merge_pieces<8>(a, rec.w, blockIdx.x, r, 0, 1));
+}
+// Few rows, many spans: a block takes rows blockIdx.y, + gridDim.y, ... of the items that
+// end in kMergeSpans spans: a warp a row where they are few pieces, else all its warps.
+// 7 us after 32 sequences' spans, 9 where 8 items of 4 rows are 228 pieces each (16 loads a
+// lane on their way; 8: 10). Blocks of 8 warps for 16 spans: 2 to 3 us more where there are
+// few pieces; one block a span and row, most of them without an item: 23.
+constexpr int kMergeSpans = 8, kFewPieces = 16, kMergeGroups = 4, kMergeWarps = 4;
+__global__ void __launch_bounds__(32 * kMergeWarps) attn_merge_spans_kernel(const __grid_constant__ AttnArgs a, const int f32) {
+    __shared__ float2 ml_sh[kMergeWarps];
+    __shared__ float4 o_sh[kMergeWarps][32];
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, last0 = (int)blockIdx.x * kMergeSpans;
+    const int end = imin(last0 + kMergeSpans, a.grid);
+    tc::pdl_wait();
+#pragma unroll 1
+    for (int last = last0 + w; last < end; last += kMergeWarps) {
+        const int4 rec = a.rec[last];
+        if (rec.x < 0 || last - rec.w >= kFewPieces) continue;
+        const Seq s = load_seq(a, rec.x);
+#pragma unroll 1
+        for (int r = (int)blockIdx.y; r < a.rows; r += kMergeGroups) {
+            const RowPlace p = row_place(a, s, rec.x, rec.y, rec.z, r);
+            if (!p.valid) break;
+            store_row(a, p, f32 != 0, merge_pieces<8>(a, rec.w, last, r, 0, 1));
         }
     }
+#pragma unroll 1
+    for (int last = last0; last < end; ++last) {
+        const int4 rec = a.rec[last];
+        if (rec.x < 0 || last - rec.w < kFewPieces) continue;
+        const Seq s = load_seq(a, rec.x);
+#pragma unroll 1
+        for (int r = (int)blockIdx.y; r < a.rows; r += kMergeGroups) {
+            const RowPlace p = row_place(a, s, rec.x, rec.y, rec.z, r);
+            if (!p.valid) break;
+            const Merged mine = merge_pieces<16>(a, rec.w, last, r, w, kMergeWarps);
+            if (lane == 0) ml_sh[w] = make_float2(mine.m, mine.l);
+            o_sh[w][lane] = mine.v;
+            __syncthreads();
+            if (w == 0) {
+                float2 ml[kMergeWarps];
+                float4 o[kMergeWarps];
 #pragma unroll
-    for (int x = 16; x; x >>= 1) l += __shfl_xor_sync(0xffffffffu, l, x);
-    if (ROW) {
-        if (lane == 0) red[4 + w] = l;
-        if (w > 0) o_sh[w - 1][lane] = v;
-        __syncthreads();
-        if (w > 0) return;
-        l = (red[4] + red[5]) + (red[6] + red[7]);
-#pragma unroll
-        for (int x = 0; x < 3; ++x) {
-            const float4 y = o_sh[x][lane];
-            v.x += y.x; v.y += y.y; v.z += y.z; v.w += y.w;
+                for (int x = 0; x < kMergeWarps; ++x) {
+                    ml[x] = ml_sh[x];
+                    o[x] = o_sh[x][lane];
+                }
+                Merged all;
+                all.add(ml, o);
+                store_row(a, p, f32 != 0, all);
+            }
+            __syncthreads();
         }
     }
-    const float inv = l == 0.f ? 0.f : 1.f / l;
-    if (4 * lane < D)
-        store_o4(a, f32 != 0, p.o + 4 * lane, make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv));
-    if (a.L && lane == 0) a.L[p.l] = l == 0.f ? -INFINITY : (ref + log2f(l)) * kLn2;
 }
 
 // ---- choice and launch ----------------------------------------------------------------
@@ -266,7 +302,8 @@ AttnPlan attn_plan(const Pool &c, int G, bool bf16, int64_t T, bool ragged, int 
     p.rows = p.kernel == AttnKernel::kSimt ? 8 : p.kernel == AttnKernel::kTc ? (per_seq > 128 ? 256 : 128)
              : bf16 && per_seq > 16        ? 32
                                            : 16;
-    int64_t grid = (int64_t)sms * (p.kernel == AttnKernel::kSimt ? 4 : p.kernel == AttnKernel::kMma ? 2 : 1);
+    const bool mma = p.kernel == AttnKernel::kMma;
+    int64_t blocks = (int64_t)sms * (p.kernel == AttnKernel::kSimt ? 4 : mma ? 2 : 1);
     // Few items of few tokens: clusters of blocks and no merge. Two blocks fit a
     // multiprocessor; a block's share stays under 4096 tokens, beyond which equal spans over
     // all multiprocessors gain more than the second launch costs.
@@ -278,9 +315,11 @@ AttnPlan attn_plan(const Pool &c, int G, bool bf16, int64_t T, bool ragged, int 
     }
     // no more spans than there can be tiles
     const int64_t tiles = ((T * G + p.rows - 1) / p.rows + c.B) * c.H *
-                          (((int64_t)c.W * c.page + kTile - 1) / kTile + 1);
-    if (grid > tiles) grid = tiles;
-    p.grid = (int)(grid < 1 ? 1 : grid > kMaxSpans ? kMaxSpans : grid);
+                          ((int64_t)c.W * c.page / (mma ? kWarpTile : kTile) + 2 + kItemTiles);
+    const int64_t workers = mma ? mma_warps(bf16, p.rows) : 1;
+    const int64_t grid = lmin(blocks * workers, lmin(tiles, kMaxSpans));
+    p.grid = (int)(grid < 1 ? 1 : grid);
+    p.blocks = (int)lmin(blocks, p.grid);
     auto up = [](size_t x) { return (x + 255) & ~(size_t)255; };
     size_t o = up(sizeof(float) * 2 * p.grid * p.rows * c.D);
     p.part_ml = o;
@@ -320,12 +359,13 @@ cudaError_t launch_attn(const AttnArgs &a, const AttnPlan &plan, bool bf16, cuda
     } else if (kernel == AttnKernel::kTc) {
         e = launch_attn_tc(a, st);
     } else {
-        e = launch_attn_mma(a, bf16, plan.cluster, st);
+        e = launch_attn_mma(a, plan, bf16, st);
     }
     if (e != cudaSuccess || plan.cluster > 1) return e;
     const int f32 = !bf16 || a.o_f32;
-    e = a.rows <= 32 ? launch_pdl(attn_merge_kernel<true>, dim3(a.grid, a.rows), dim3(128), st, a, f32)
-                     : launch_pdl(attn_merge_kernel<false>, dim3(a.grid, a.rows / 4), dim3(128), st, a, f32);
+    const unsigned groups = (unsigned)(a.grid + kMergeSpans - 1) / kMergeSpans;
+    e = a.rows <= 32 ? launch_pdl(attn_merge_spans_kernel, dim3(groups, kMergeGroups), dim3(32 * kMergeWarps), st, a, f32)
+                     : launch_pdl(attn_merge_rows_kernel, dim3(a.grid, a.rows / 4), dim3(128), st, a, f32);
     if (e != cudaSuccess) return e;
     note_launch();
     return cudaGetLastError();

@@ -159,7 +159,7 @@ struct Piece {
     __device__ __forceinline__ bool next(const AttnArgs &a) {
         cur.tiles_left -= k1 - k0;
         if (cur.tiles_left <= 0) return false;
-        next_item(a, cur);
+        next_item<kTile>(a, cur);
         return set();
     }
 };
@@ -172,7 +172,6 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
     constexpr bool SEP = C::SEP;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    __shared__ int64_t scan_sh[16];
     __shared__ Cursor cur_sh;
     const uint32_t sbase = smem_u32(smem);
     const uint32_t bar0 = sbase + C::BAR_OFF;
@@ -230,8 +229,14 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
         tmem_alloc(smem_u32(tmem_slot), 512);
         tmem_relinquish();
     }
-    const Span sp = find_span<512>(a, cta, scan_sh, &cur_sh);
-    if (threadIdx.x == 0) write_record(a, sp, cur_sh, cta);
+    {
+        Cursor at;
+        const Span sp = find_spans<512, 1, kTile>(a, at);
+        if (threadIdx.x == 0) {
+            cur_sh = at;
+            write_record(a, sp, at, cta);
+        }
+    }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();

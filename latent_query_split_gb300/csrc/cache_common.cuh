@@ -66,7 +66,8 @@ struct AppendArgs {
 enum class AttnKernel { kSimt, kMma, kTc };
 struct AttnPlan {
     AttnKernel kernel;
-    int rows, grid;
+    int rows, grid;                     // rows of a tile; spans at most
+    int blocks;                         // that share the spans (where a block has several)
     int cluster;                        // blocks an item where the call takes one launch (1: spans and a merge)
     size_t part_ml, rec, bytes;         // workspace: part_O at 0
 };
@@ -88,7 +89,8 @@ struct SharedMemoryLimit {
 };
 
 cudaError_t launch_attn(const AttnArgs &a, const AttnPlan &plan, bool bf16, cudaStream_t st);
-cudaError_t launch_attn_mma(const AttnArgs &a, bool bf16, int cluster, cudaStream_t st);
+cudaError_t launch_attn_mma(const AttnArgs &a, const AttnPlan &plan, bool bf16, cudaStream_t st);
+constexpr int mma_warps(bool bf16, int rows) { return bf16 && rows == 16 ? 6 : 4; }     // of a block
 cudaError_t launch_attn_tc(const AttnArgs &a, cudaStream_t st);
 cudaError_t launch_append(const AppendArgs &a, bool bf16, cudaStream_t st);
 

@@ -37,6 +37,7 @@ struct Cursor {
 struct Span {
     int64_t begin, total;
     int parts;                           // spans in use
+    int part;                            // this worker's
 };
 
 // One block-wide sum (and exclusive prefix) of an int64 per thread.
@@ -62,70 +63,81 @@ __device__ __forceinline__ int64_t block_scan(int64_t v, int64_t *sh, int64_t &t
     return base + x - v;
 }
 
-// The span of CTA `c` and the cursor at its first tile. Every thread of the
-// block calls it; sh: NT / 32 int64, found: one Cursor, in shared memory.
-// An empty span leaves tiles_left = 0.
-template <int NT>
-static __device__ __noinline__ Span find_span(const AttnArgs &a, int c, int64_t *sh, Cursor *found) {
+// The spans of this block's NS workers, w gridDim.x + blockIdx.x (so that few spans are on
+// many multiprocessors), and a cursor at the first tile of each. Every thread of the block calls it and gets
+// those of worker threadIdx.x / 32 (of the only one where NS = 1); an empty span leaves
+// tiles_left = 0. One pass over the sequences for the tiles in all, one (none where a
+// thread has one sequence at most) to find the spans' first ones.
+template <int NT, int NS, int TILE>
+static __device__ __noinline__ Span find_spans(const AttnArgs &a, Cursor &cur) {
+    __shared__ int64_t sh[NT / 32], begin_sh[NS], end_sh[NS], at_sh[NS];
+    __shared__ int b_sh[NS];
     const int tid = threadIdx.x, B = a.c.B;
     Span sp;
     sp.total = 0;
-    int64_t first = 0;                   // this thread's tiles in the first block of sequences
+    int64_t first = 0, at = 0, sum;      // this thread's tiles in the first block of sequences, those before them
 #pragma unroll 1
     for (int base = 0; base < B; base += NT) {
-        int64_t v = 0, sum;
+        int64_t v = 0;
         if (base + tid < B) {
             const Seq s = load_seq(a, base + tid);
-            if (!s.ok && c == 0) flag_bad(a.status);
-            v = seq_tiles(s, a.G, a.rows, a.causal) * a.c.H;
+            if (!s.ok && blockIdx.x == 0) flag_bad(a.status);
+            v = seq_tiles(s, a.G, a.rows, a.causal, TILE) * a.c.H;
         }
-        if (base == 0) first = v;
-        block_scan<NT>(v, sh, sum);
+        const int64_t before = block_scan<NT>(v, sh, sum);
+        if (base == 0) {
+            first = v;
+            at = before;
+        }
         sp.total += sum;
     }
     sp.parts = (int)lmin(a.grid, sp.total);
-    if (tid == 0) found->tiles_left = 0;
-    if (c >= sp.parts) {
-        sp.begin = sp.total;
-        __syncthreads();
-        return sp;
-    }
-    sp.begin = span_begin(sp.total, sp.parts, c);
-    const int64_t end = span_begin(sp.total, sp.parts, c + 1);
-    int64_t before = 0;
-#pragma unroll 1
-    for (int base = 0; base < B; base += NT) {
-        int64_t v = first, sum;
-        if (base > 0) {
-            v = 0;
-            if (base + tid < B) v = seq_tiles(load_seq(a, base + tid), a.G, a.rows, a.causal) * a.c.H;
-        }
-        int64_t at = before + block_scan<NT>(v, sh, sum);
-        if (v > 0 && at <= sp.begin && sp.begin < at + v) {
-            Cursor cur;
-            cur.b = base + tid;
-            cur.s = load_seq(a, cur.b);
-            cur.rt = 0;
-            while (true) {
-                cur.nt = item_tiles(cur.s, a.G, a.rows, cur.rt, a.causal);
-                if (sp.begin < at + (int64_t)cur.nt * a.c.H) break;
-                at += (int64_t)cur.nt * a.c.H;
-                ++cur.rt;
-            }
-            const int64_t off = sp.begin - at;
-            cur.h = (int)(off / cur.nt);
-            cur.k = (int)(off - (int64_t)cur.h * cur.nt);
-            cur.tiles_left = (int)(end - sp.begin);
-            *found = cur;
-        }
-        before += sum;
-        if (before > sp.begin) break;    // the same for every thread
+    const int w = NS > 1 ? tid >> 5 : 0;
+    sp.part = w * (int)gridDim.x + (int)blockIdx.x;
+    if (tid < NS) {
+        const int c = tid * (int)gridDim.x + (int)blockIdx.x;
+        begin_sh[tid] = c < sp.parts ? span_begin(sp.total, sp.parts, c) : -1;
+        end_sh[tid] = c < sp.parts ? span_begin(sp.total, sp.parts, c + 1) : -1;
     }
     __syncthreads();
+    int64_t past = 0;                    // tiles of the blocks of sequences before this one
+#pragma unroll 1
+    for (int base = 0; base < B; base += NT) {
+        int64_t v = first;
+        if (B > NT) {
+            if (base > 0) v = base + tid < B ? seq_tiles(load_seq(a, base + tid), a.G, a.rows, a.causal, TILE) * a.c.H : 0;
+            at = past + block_scan<NT>(v, sh, sum);
+            past += sum;
+        }
+#pragma unroll
+        for (int x = 0; x < NS; ++x)
+            if (at <= begin_sh[x] && begin_sh[x] < at + v) {
+                b_sh[x] = base + tid;
+                at_sh[x] = at;
+            }
+    }
+    __syncthreads();
+    sp.begin = begin_sh[w];
+    cur.tiles_left = (int)(end_sh[w] - sp.begin);
+    if (cur.tiles_left > 0) {
+        int64_t off = sp.begin - at_sh[w];
+        cur.b = b_sh[w];
+        cur.s = load_seq(a, cur.b);
+        cur.rt = 0;
+        while (true) {
+            cur.nt = item_tiles(cur.s, a.G, a.rows, cur.rt, a.causal, TILE);
+            if (off < (int64_t)cur.nt * a.c.H) break;
+            off -= (int64_t)cur.nt * a.c.H;
+            ++cur.rt;
+        }
+        cur.h = (int)(off / cur.nt);
+        cur.k = (int)(off - (int64_t)cur.h * cur.nt);
+    }
     return sp;
 }
 
 // The next item after `cur` (called only while tiles of the span are left).
+template <int TILE>
 static __device__ __noinline__ void next_item(const AttnArgs &a, Cursor &cur) {
     cur.k = 0;
     if (++cur.h < a.c.H) return;
@@ -136,7 +148,7 @@ static __device__ __noinline__ void next_item(const AttnArgs &a, Cursor &cur) {
         cur.s = load_seq(a, cur.b);
         cur.rt = 0;
     }
-    cur.nt = item_tiles(cur.s, a.G, a.rows, cur.rt, a.causal);
+    cur.nt = item_tiles(cur.s, a.G, a.rows, cur.rt, a.causal, TILE);
 }
 
 // Which item's last piece CTA c holds, for the merge: (b, rt, h, first CTA),

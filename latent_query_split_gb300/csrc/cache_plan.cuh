@@ -16,7 +16,9 @@ namespace flare {
 namespace cache {
 
 constexpr int kTile = 128;       // tokens of one tile of the attention's work
-constexpr int kMaxSpans = 1024;  // spans of a call at most
+constexpr int kWarpTile = 32;    // the same where every warp has a span of its own; there an item
+constexpr int kItemTiles = 4;    // counts so many more, without tokens: the time it takes to begin one
+constexpr int kMaxSpans = 2048;  // spans of a call at most
 
 FLARE_HD int imin(int a, int b) { return a < b ? a : b; }
 FLARE_HD int imax(int a, int b) { return a > b ? a : b; }
@@ -72,18 +74,19 @@ FLARE_HD int limit_of(const Seq &s, int i, bool causal) {
 }
 // Tiles of one (row tile, head): one at least, so that somebody writes the
 // rows that see nothing.
-FLARE_HD int item_tiles(const Seq &s, int G, int rows, int rt, bool causal) {
-    return imax(1, (int)((unsigned)(visible(s, G, rows, rt, causal) + kTile - 1) / kTile));
+FLARE_HD int item_tiles(const Seq &s, int G, int rows, int rt, bool causal, int tile = kTile) {
+    const int n = imax(1, (int)((unsigned)(visible(s, G, rows, rt, causal) + tile - 1) / (unsigned)tile));
+    return tile == kWarpTile ? n + kItemTiles : n;
 }
 // Tiles of one head over the row tiles of a sequence.
-FLARE_HD int64_t seq_tiles(const Seq &s, int G, int rows, bool causal) {
+FLARE_HD int64_t seq_tiles(const Seq &s, int G, int rows, bool causal, int tile = kTile) {
     const int m = row_tiles(s, G, rows);
-    if (!causal) return m > 0 ? (int64_t)m * item_tiles(s, G, rows, 0, false) : 0;
+    if (!causal) return m > 0 ? (int64_t)m * item_tiles(s, G, rows, 0, false, tile) : 0;
     int64_t sum = 0;
 #ifdef __CUDACC__
 #pragma unroll 1
 #endif
-    for (int rt = 0; rt < m; ++rt) sum += item_tiles(s, G, rows, rt, true);
+    for (int rt = 0; rt < m; ++rt) sum += item_tiles(s, G, rows, rt, true, tile);
     return sum;
 }
 
