@@ -229,7 +229,11 @@ size_t flare_cache_workspace_bytes(const flare_cache_dims_t *dims, int64_t T) {
         fail(FLARE_ERR_INVALID_ARG, "Hq=%d, T=%lld: no query rows", dims->Hq, (long long)T);
         return (size_t)-1;
     }
-    return T == 0 || dims->B == 0 ? 0 : plan_for(dims, dims->Hq / dims->H, T, true).bytes;
+    if (T == 0 || dims->B == 0) return 0;
+    // equal sequences and ragged ones may be cut differently
+    const size_t ragged = plan_for(dims, dims->Hq / dims->H, T, true).bytes;
+    const size_t equal = plan_for(dims, dims->Hq / dims->H, T, false).bytes;
+    return ragged > equal ? ragged : equal;
 }
 
 flare_status_t flare_cache_attn(const flare_cache_dims_t *dims, const flare_cache_t *cache, const void *Q,

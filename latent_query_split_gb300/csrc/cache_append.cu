@@ -616,7 +616,10 @@ cudaError_t launch_append(const AppendArgs &args, bool bf16, cudaStream_t st) {
             append_kernel<true><<<grid, 256, 0, st>>>(a);
         else
             append_kernel<false><<<grid, 256, 0, st>>>(a);
-    } else if (a.T <= 8 * (int64_t)a.c.B) {
+    } else if (a.c.B > 8 && a.T <= 8 * (int64_t)a.c.B) {
+        // (8 cache and 32 query heads of 128, us by warps and by pages: 1 sequence of 1 token 5.8
+        // and 4.8, 8 of 8 9.2 and 5.8, 16 of 1 5.9 and 7.6, 16 of 8 9.1 and 8.8, 32 of 1 6.0 and
+        // 10.8, of 8 9.4 and 14.5, of 16 14.6 and 14.8)
         const dim3 grid((unsigned)slots, (a.c.H + (a.Hq + kQHeads - 1) / kQHeads + 7) / 8);
         if (bf16) {
             if (a.inter) append_token_kernel<true, true><<<grid, 256, 0, st>>>(a);

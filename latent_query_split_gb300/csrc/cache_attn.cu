@@ -294,28 +294,51 @@ __global__ void __launch_bounds__(32 * kMergeWarps) attn_merge_spans_kernel(cons
 }
 
 // ---- choice and launch ----------------------------------------------------------------
+// The rules below are of sizes that the host knows: R rows a sequence and head, the room
+// W * page of the table. Times in us of replayed graphs on one GPU of 152 multiprocessors,
+// 8 heads, bf16, D = 128 where nothing else is said.
+//
+// R > 32, and R > 16 over more than 16,384 tokens: tcgen05 (D = 64 or 128), else mma.sync.
+// 2 sequences of 65,536 tokens: 16 rows 72 by mma.sync, 17 88 and by tcgen05 83, 32 102 and
+// 85, 64 155 and 88 (D = 64: 17 78 and 62, 64 127 and 65). Of fewer tokens the larger block
+// takes longer to begin: 32 rows of 6 sequences of 1,000 19 and 30, of 64 of 500 65 and 72,
+// of 6 of 9,000 56 and 53, 33 rows of 64 of 500 (64 rows by mma.sync) 72 by tcgen05.
+//
+// Tiles of 256 rows by tcgen05 read the cache once for both halves, 128 rows pad less: 384
+// rows 203 by 128 and 259 by 256, 512 257 and 260, 1,024 481 and 474; D = 64: 256 110 and
+// 111, 384 153 and 186, 512 196 and 187, 1,024 368 and 342. So 256 where that pads by no
+// more than a sixteenth (ragged: half a tile a sequence), for D = 128 from 512 rows on.
+static int tc_rows(int64_t R, int D, bool ragged) {
+    if (R <= (D == 128 ? 512 : 128)) return 128;
+    if (ragged) return R > 896 ? 256 : 128;
+    return (R + 255) / 256 * 240 <= (R + 127) / 128 * 128 ? 256 : 128;
+}
 AttnPlan attn_plan(const Pool &c, int G, bool bf16, int64_t T, bool ragged, int family, int sms) {
     AttnPlan p;
     p.kernel = family == FLARE_KERNEL_SIMT ? AttnKernel::kSimt : AttnKernel::kMma;
-    const int64_t per_seq = c.B > 0 ? T * G / c.B : 0;      // rows of a head and sequence on average
-    if (p.kernel == AttnKernel::kMma && bf16 && (c.D == 64 || c.D == 128) && per_seq > 32) p.kernel = AttnKernel::kTc;
-    p.rows = p.kernel == AttnKernel::kSimt ? 8 : p.kernel == AttnKernel::kTc ? (per_seq > 128 ? 256 : 128)
+    const int64_t per_seq = c.B > 0 ? T * G / c.B : 0;      // R, on average
+    const int64_t room = (int64_t)c.W * c.page;
+    if (p.kernel == AttnKernel::kMma && bf16 && (c.D == 64 || c.D == 128) && per_seq > (room > 16384 ? 16 : 32))
+        p.kernel = AttnKernel::kTc;
+    p.rows = p.kernel == AttnKernel::kSimt ? 8 : p.kernel == AttnKernel::kTc ? tc_rows(per_seq, c.D, ragged)
              : bf16 && per_seq > 16        ? 32
                                            : 16;
     const bool mma = p.kernel == AttnKernel::kMma;
     int64_t blocks = (int64_t)sms * (p.kernel == AttnKernel::kSimt ? 4 : mma ? 2 : 1);
-    // Few items of few tokens: clusters of blocks and no merge. Two blocks fit a
-    // multiprocessor; a block's share stays under 4096 tokens, beyond which equal spans over
-    // all multiprocessors gain more than the second launch costs.
+    // Few items of few tokens: clusters of 2 to 8 blocks an item and no merge. Two blocks fit
+    // a multiprocessor; spans use all warps of all of them, and win beyond 2,048 tokens a
+    // block where clusters leave most idle, 4,096 where they do not. One token, 4 queries a
+    // head, by clusters and by spans: 500 tokens 7.2 and 11.6, 16,000 25.6 and 24.2, 32,000
+    // 42.7 and 28.7; 4 sequences of 30,000 50 and 55, 16 of 8,000 52 and 58.
     p.cluster = 1;
-    if (p.kernel == AttnKernel::kMma && !ragged && c.B > 0) {
+    if (mma && !ragged && c.B > 0) {
         const int64_t items = (T / c.B * G + p.rows - 1) / p.rows * c.B * c.H;
         for (int s = 8; s > 1 && p.cluster == 1; s /= 2)
-            if (items * s <= 2 * sms && (int64_t)c.W * c.page <= 4096 * s) p.cluster = s;
+            if (items * s <= 2 * sms && room <= (items * s > sms ? 4096 : 2048) * s) p.cluster = s;
     }
     // no more spans than there can be tiles
     const int64_t tiles = ((T * G + p.rows - 1) / p.rows + c.B) * c.H *
-                          ((int64_t)c.W * c.page / (mma ? kWarpTile : kTile) + 2 + kItemTiles);
+                          (room / (mma ? kWarpTile : kTile) + 2 + kItemTiles);
     const int64_t workers = mma ? mma_warps(bf16, p.rows) : 1;
     const int64_t grid = lmin(blocks * workers, lmin(tiles, kMaxSpans));
     p.grid = (int)(grid < 1 ? 1 : grid);

@@ -91,6 +91,19 @@ def test_attn_refuses(lib, kw):
     assert _attn(lib, _dims(), **kw) == INVALID
 
 
+@pytest.mark.parametrize("D,dtype", [(64, flare.FLARE_BF16), (128, flare.FLARE_BF16), (96, flare.FLARE_BF16), (128, flare.FLARE_F32)])
+def test_the_workspace_is_enough_for_equal_and_ragged_rows(lib, D, dtype):
+    """What the query names passes the size check of either form of the call (the
+    address, which is checked next, is refused: nothing is launched)."""
+    for W in (8, 1024):
+        for n in (1, 5, 8, 9, 16, 17, 32, 33, 64, 65, 75, 128, 192, 193, 256, 257, 320, 448, 449, 512, 1000, 4096):
+            d = _dims(D=D, dtype=dtype, W=W)
+            need = lib.flare_cache_workspace_bytes(bytes(d), 2 * n)
+            for cu in (None, A[12]):
+                assert _attn(lib, d, T=2 * n, cu=cu, ws=(1 << 40) + 64, wsb=need) == INVALID, (W, n, cu)
+                assert "256-byte" in lib.flare_last_error_string().decode()
+
+
 def test_attn_needs_its_workspace_and_query_heads(lib):
     need = lib.flare_cache_workspace_bytes(bytes(_dims()), 4)
     assert need > 0

@@ -71,7 +71,8 @@ def starts(counts):
 
 def check_attn(O, L, Q, cache, lens, counts, causal, scale=None, kernel="auto", o_f32=False):
     T, Hq, D = Q.shape
-    many = D in (64, 128) and T * Hq // (cache.k.shape[1] * len(lens)) > 32
+    room = cache.page_table.shape[1] * cache.k.shape[2]
+    many = D in (64, 128) and T * Hq // (cache.k.shape[1] * len(lens)) > (16 if room > 16384 else 32)
     step = 0.0 if kernel == "simt" or Q.dtype == torch.float32 else 2.0 ** -8 if many else 2.0 ** -11
     ref = cache_ref.host(cache)
     o, l, A, E = cache_ref.attn(ref, Q.cpu(), lens, counts, causal, scale)
@@ -331,6 +332,32 @@ def test_append_many_sequences():
     check_append(cache, before, K, V, None, lens, counts, freqs(16), False, out, None)
 
 
+@pytest.mark.parametrize("dtype,H,Hq,D,page,rot,inter", [
+    ("bf16", 2, 18, 128, 32, 128, False), ("fp32", 9, 9, 96, 16, 32, True), ("bf16", 1, 0, 16, 16, 0, False),
+    ("fp32", 3, 6, 64, 128, 64, False), ("bf16", 4, 4, 112, 64, 16, True),
+])
+def test_append_few_tokens_of_more_than_eight_sequences(dtype, H, Hq, D, page, rot, inter):
+    """Step after step, magnitudes growing and shrinking from one to the next, some
+    channels not finite: a warp a page and head."""
+    g = torch.Generator().manual_seed(71)
+    B = 11
+    lens = torch.randint(0, 3 * page, (B,), generator=g).tolist()
+    cache = make_cache(B, 5, H, D, page)
+    fill(cache, lens, seed=72)
+    f = freqs(rot)
+    for size in (1.0, 2.0 ** 9, 2.0 ** -6):
+        counts = torch.randint(0, 9, (B,), generator=g).tolist()
+        before = cache_ref.host(cache)
+        T = sum(counts)
+        K, V = ((size * torch.randn((T, H, D), generator=g)).to(DT[dtype]) for _ in range(2))
+        K[T // 2, 0, D - 1], V[T // 3, H - 1, 0] = math.inf, math.nan
+        Q = torch.randn((T, Hq, D), generator=g).to(DT[dtype]).cuda() if Hq else None
+        out, q = run_append(cache, K.cuda(), V.cuda(), Q, lens, counts, f, inter)
+        flare.flare_device_status()
+        check_append(cache, before, K, V, Q, lens, counts, f, inter, out, q)
+        lens = out.tolist()
+
+
 # ---- attention -----------------------------------------------------------------------
 ATTNS = [  # dtype, H, G, D, page, lens, counts, causal
     ("bf16", 2, 4, 128, 64, [1500], [1], True),
@@ -538,6 +565,90 @@ def test_attn_scores_that_grow(kernel, D, n):
         Q = torch.randn((n, H, D), generator=torch.Generator().manual_seed(seed)).bfloat16().cuda()
         O, L = flare.flare_cache_attn(Q, cache, ints(lens), cu_seqlens=ints([0, n]), causal=False, kernel=kernel, scale=0.02)
         check_attn(O, L, Q, cache, lens, [n], False, scale=0.02, kernel=kernel)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_attn_wide_row_tiles(D):
+    """Row tiles of 256 (ragged calls of more than 896 rows a sequence on average): the
+    causal edge inside tiles, a sequence that ends inside one, keys that double."""
+    page, lens, counts = 64, [1300, 950, 3], [1250, 949, 600]
+    cache = make_cache(3, 21, 1, D, page)
+    fill(cache, lens, seed=65)
+    Q = torch.randn((sum(counts), 1, D), generator=torch.Generator().manual_seed(66)).bfloat16().cuda()
+    O, L = flare.flare_cache_attn(Q, cache, ints(lens), cu_seqlens=starts(counts))
+    flare.flare_device_status()
+    check_attn(O, L, Q, cache, lens, counts, True)
+    for w in range(20):
+        cache.k_scale[int(cache.page_table[0, w])] = 2.0 ** (w - 18)
+    O, L = flare.flare_cache_attn(Q, cache, ints(lens), cu_seqlens=starts(counts), causal=False, scale=0.02)
+    check_attn(O, L, Q, cache, lens, counts, False, scale=0.02)
+
+
+@pytest.mark.parametrize("D,n", [(64, 20), (128, 17), (128, 32)])
+def test_attn_some_rows_over_a_long_table(D, n):
+    """17 to 32 rows a sequence where the table has room for more than 16,384 tokens."""
+    page, lens = 128, [700, 0, 1, 129]
+    cache = make_cache(4, 130, 1, D, page)
+    fill(cache, lens, seed=67)
+    Q = torch.randn((4, n, 1, D), generator=torch.Generator().manual_seed(68)).bfloat16().cuda()
+    for causal in (True, False):
+        O, L = flare.flare_cache_attn(Q, cache, ints(lens), causal=causal)
+        check_attn(O, L, Q.reshape(4 * n, 1, D), cache, lens, [n] * 4, causal)
+
+
+@pytest.mark.parametrize("M,D", [(3, 64), (40, 64), (150, 64), (64, 128), (200, 128), (700, 128)])
+def test_rows_that_one_token_fills(M, D):
+    """A late token whose score is far above all others': Z (fp32) is its value. The
+    weights' rounding (2^-8 or 2^-11) must not show in it: of the others' share r of the
+    row at most 2^-7 r max|v| of it can, on top of the bounds above."""
+    H, page, lens = 1, 64, [900]
+    cache = make_cache(1, 16, H, D, page)
+    fill(cache, lens, seed=69)
+    g = torch.Generator().manual_seed(70)
+    Q = (0.1 * torch.randn((H, M, D), generator=g)).abs().bfloat16().cuda()
+    p, s = int(cache.page_table[0, 13]), 17                               # token 849
+    cache.k_scale[p] = 2.0 ** -4
+    cache.k.view(torch.uint8)[p, 0, s] = torch.full((D,), 400.0).to(cache_ref.F8).view(torch.uint8).cuda()
+    Z, L = flare.flare_cache_encoder_fwd(Q, cache, ints(lens))
+    q = Q[0][:, None]
+    o, l, A, E = cache_ref.attn(cache_ref.host(cache), q.cpu(), lens, [M], False, None)
+    v = cache.v[p, 0, s].double().cpu() * cache.v_scale[p, 0].double().cpu()
+    big = max((cache.v[int(x), 0, :].double().cpu().nan_to_num().abs().max() * cache.v_scale[int(x), 0].double().cpu()).item()
+              for x in cache.page_table[0, :15])
+    k = cache.k[p, 0, s].double().cpu() * cache.k_scale[p, 0].double().cpu()
+    rest = 1 - torch.exp((q.double().cpu()[:, 0] @ k) * D ** -0.5 - l[:, 0])                      # share of the other tokens
+    assert rest.max() < 2.0 ** -6                 # (the bound below is of `rest`, and holds for any: this is for its sharpness)
+    e = (D + 8) * 2.0 ** -23 * E[:, 0] + 2.0 ** -20
+    tol = (2 * rest[:, None] * e[:, None] + 900 * 2.0 ** -23) * A[:, 0] + 2.0 ** -7 * rest.clamp(min=0)[:, None] * big + 1e-9 * big
+    worst = ((Z[0, 0].double().cpu() - o[:, 0]).abs() / tol).max().item()
+    assert worst <= 1, f"Z is {worst:.3g} of its bound off"
+    assert ((o[:, 0] - v).abs() <= 2 * rest[:, None].clamp(min=0) * big + 1e-12 * big).all()
+
+
+@pytest.mark.parametrize("dtype,G", [("bf16", 4), ("bf16", 11), ("fp32", 2)])
+def test_attn_short_and_empty_sequences_among_long_ones(dtype, G):
+    """Items of no tile at all, of one and of many: spans begin and end inside them."""
+    H, D, page, B = 2, 64, 32, 60
+    g = torch.Generator().manual_seed(73)
+    lens = [0 if i % 4 == 0 else int(x) for i, x in enumerate(torch.randint(0, 40, (B,), generator=g) ** 2 % 1500)]
+    lens[7], lens[-1], lens[-2], lens[-3] = 5000, 0, 0, 0
+    cache = make_cache(B, 160, H, D, page, spare=1)
+    fill(cache, lens, seed=74)
+    Q = torch.randn((B, H * G, D), generator=g).to(DT[dtype]).cuda()
+    O, L = flare.flare_cache_attn(Q, cache, ints(lens), cu_seqlens=starts([1] * B))
+    flare.flare_device_status()
+    check_attn(O, L, Q, cache, lens, [1] * B, True)
+
+
+@pytest.mark.parametrize("dtype,D", [("bf16", 128), ("fp32", 32)])
+def test_attn_one_item_over_every_span(dtype, D):
+    """One head of one long sequence: as many pieces as there are spans."""
+    page, lens = 128, [70_001]
+    cache = make_cache(1, 548, 1, D, page)
+    fill(cache, lens, seed=75)
+    Q = torch.randn((1, 2, 3, D), generator=torch.Generator().manual_seed(76)).to(DT[dtype]).cuda()
+    O, L = flare.flare_cache_attn(Q, cache, ints(lens))
+    check_attn(O, L, Q[0], cache, lens, [2], True)
 
 
 @pytest.mark.parametrize("dtype,n", [("bf16", 1), ("bf16", 130), ("fp32", 1)])
