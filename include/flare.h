@@ -421,7 +421,9 @@ FLARE_API size_t flare_cache_workspace_bytes(const flare_cache_dims_t *dims, int
  * Rows of Q behind the last sequence are not read and theirs of O and L keep
  * what they hold. A token on a page number outside the pool is not seen, and
  * the device status is set. Softmax and sums are fp32; the kernels for bf16
- * round the weights exp(S - max) to fp16 where they meet the values.
+ * round the weights exp(S - ref) where they meet the values: to fp16 for few
+ * rows of a sequence and shared head, to bf16 for many, where O is then divided
+ * by the sum of the rounded ones (L is of the exact ones).
  * workspace: flare_cache_workspace_bytes(dims, T) bytes, 256-byte aligned
  * (equal sequences of few rows over few tokens need none: such a call succeeds
  * with NULL, where others return FLARE_ERR_WORKSPACE).

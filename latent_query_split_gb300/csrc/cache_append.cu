@@ -425,6 +425,8 @@ __global__ void __launch_bounds__(256, TPT == 1 ? 3 : TPT == 2 ? 2 : 1) append_p
 // ---- a token or a few a sequence: one warp a touched page and head ------------------
 // What counts is latency: a warp reads its head's keys and values once for the
 // scale and once (from the caches) for the codes. Eight query heads are one warp's.
+// 96 tokens of 96 sequences, 8 cache and 32 query heads of 128 (1.3 MB): 6.7 us, which
+// are the launch, three dependent reads (lengths and page, tokens, scale) and a write.
 constexpr int kQHeads = 8;
 template <bool BF16, bool INTER>
 __global__ void __launch_bounds__(256) append_token_kernel(const AppendArgs a) {
@@ -511,6 +513,8 @@ __global__ void __launch_bounds__(256) append_token_kernel(const AppendArgs a) {
 }
 
 // ---- any alignment, any even number of rotated channels -----------------------------
+// An element a thread, two passes over the tokens. For what the kernels above cannot
+// take: 4 sequences of 2,000 tokens (8 and 32 heads of 128) 858 us, where theirs is 48.
 // One block a touched page and head: the largest new magnitude, the scale, the
 // old codes if it grew, the new codes; keys, then values.
 template <bool BF16>

@@ -15,8 +15,10 @@ namespace cache {
 // token a lane for S = Q K^T (a lane reads its whole key row, 16 bytes at a
 // time; Q is broadcast from shared memory), then four channels a lane for
 // O += P V (a warp reads a value row, 4 bytes a lane). Every product is an
-// fp32 FMA on exactly converted codes. The reads are as few as they can be
-// for one head's rows; the FMAs bound it from some four rows on.
+// fp32 FMA on exactly converted codes. Called by name only (kernel = SIMT): the
+// plainest form, that the others can be held against. Bound by latency (a lane's
+// whole key row, then the values, in turn): 8 sequences of 8,000 tokens with 8 heads
+// of 128 and 1 to 8 queries each 190 us, where the tensor kernels take 30 to 42.
 template <int R, bool BF16>
 __global__ void __launch_bounds__(128) attn_simt_kernel(const __grid_constant__ AttnArgs a) {
     constexpr int NT = 128, NW = 4;

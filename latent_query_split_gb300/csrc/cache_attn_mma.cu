@@ -589,7 +589,9 @@ __global__ void __launch_bounds__(C::NT, 2) attn_mma_span_kernel(const __grid_co
 // A cluster of blocks takes one item, each warp of them an equal share of its units, and
 // joins their states through shared memory and distributed shared memory: one launch and
 // no workspace, for calls so small that a second launch would cost as much as the
-// attention.
+// attention. One token of 4 queries a head, 8 heads of 128, 1,500 tokens: 8.1 us; 3 tokens
+// of 5 queries, 6 sequences of 2 to 9,000, 4 heads of 64: 18.5 (the longest sequence's 563
+// units are 12 rounds of its 48 warps); float32, 500 to 7,000 tokens, 4 heads of 64: 14.5.
 // The states of a block's warps become one: sink(r, d, M, l, v) gets channels d .. d + 3 of
 // row r, with reference M and sum l. `at`: shared memory (JOIN bytes) that the warps may
 // have used until now.

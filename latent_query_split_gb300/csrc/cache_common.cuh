@@ -39,10 +39,10 @@ struct AttnArgs {
     int o_f32;                          // O is fp32 although Q is bf16
     int rows;                           // rows of one row tile
     int grid;                           // spans at most
-    // workspace: a span's unfinished pieces, two at most (see write_piece)
+    // workspace: a span's unfinished pieces, two at most: [1] begins its item, [0] does not
     float *part_O;                      // [grid][2][rows][D]
     float2 *part_ml;                    // [grid][2][rows]
-    int4 *rec;                          // [grid][2]: the item whose last piece a span holds
+    int4 *rec;                          // [grid]: the item whose last piece a span holds
     unsigned *status;
 };
 

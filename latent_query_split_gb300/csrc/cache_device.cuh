@@ -3,10 +3,10 @@
 // pages of its tokens, and where its results go.
 //
 // Work: the items (sequence b, row tile rt, cache head h), in that order with
-// h innermost, are each cut into tiles of kTile tokens; the tiles of all items
-// in a row are dealt out to the workers (CTAs) in equal contiguous spans, so
+// h innermost, are each cut into tiles of tokens; the tiles of all items in a row
+// are dealt out to the workers (blocks, or warps) in equal contiguous spans, so
 // that one long sequence among short ones is shared by all of them. Lengths
-// are device data: every CTA adds up the tiles for itself (one pass over the
+// are device data: every block adds up the tiles for itself (one pass over the
 // B lengths). An item that lies in one span is finished there; one that is cut
 // leaves a partial (O, m, l) in each span and the merge kernel adds them up.
 #pragma once
