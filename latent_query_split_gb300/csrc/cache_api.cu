@@ -153,6 +153,7 @@ flare_status_t append_run(const flare_cache_dims_t *d, const flare_cache_t *cach
     if ((s = check_rows(d, T, lens, cu)) != FLARE_OK) return s;
     if ((Q == nullptr) != (Q_out == nullptr))
         return fail(FLARE_ERR_INVALID_ARG, "Q and Q_out must be given together");
+    if (Q && Q == Q_out) return fail(FLARE_ERR_INVALID_ARG, "Q_out may not be Q");
     if (Q && d->Hq < 1) return fail(FLARE_ERR_INVALID_ARG, "queries need Hq >= 1");
     if (d->B == 0) return FLARE_OK;
     if (T > 0 && (!K || !V)) return fail(FLARE_ERR_INVALID_ARG, "NULL tensor");

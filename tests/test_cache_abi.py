@@ -80,7 +80,8 @@ def test_cache_pointers_are_checked(lib, name):
 
 @pytest.mark.parametrize("kw", [dict(K=None), dict(V=None), dict(T=-1), dict(T=5), dict(lens=None), dict(lens=A[7] + 2),
                                 dict(Q=None), dict(Qo=None), dict(ks=127), dict(vs=-128), dict(qs=255), dict(rot=63),
-                                dict(rot=0), dict(rot=66), dict(out=A[7]), dict(K=A[5] + 1), dict(f=A[10] + 1), dict(T=1 << 31)])
+                                dict(rot=0), dict(rot=66), dict(out=A[7]), dict(Qo=A[8]), dict(K=A[5] + 1), dict(f=A[10] + 1),
+                                dict(T=1 << 31)])
 def test_append_refuses(lib, kw):
     assert _append(lib, _dims(), **kw) == INVALID
 
