@@ -134,23 +134,44 @@ struct Task {
     float c[8], s[8];
 };
 template <bool INTER>
-__device__ __forceinline__ void make_task(const AppendArgs &a, const Slot &x, int id, Task &k, const uint64_t *freq) {
+__device__ __forceinline__ void place_task(const AppendArgs &a, int id, Task &k) {
     const int per = a.c.D >> 4;
     k.t = id / per;
     k.p = id - k.t * per;
     k.turned = 16 * k.p < a.rot;
     k.a = !INTER && k.turned ? 8 * k.p : 16 * k.p;
     k.b = !INTER && k.turned ? a.rot / 2 + 8 * k.p : 16 * k.p + 8;
+}
+__device__ __forceinline__ void turn_task(const Slot &x, Task &k, const uint64_t *freq) {
     if (k.turned)
 #pragma unroll
         for (int i = 0; i < 8; ++i) sincos_at(x.pos + k.t, freq[8 * k.p + i], k.s[i], k.c[i]);
+}
+template <bool INTER>
+__device__ __forceinline__ void make_task(const AppendArgs &a, const Slot &x, int id, Task &k, const uint64_t *freq) {
+    place_task<INTER>(a, id, k);
+    turn_task(x, k, freq);
+}
+template <bool L1>
+__device__ __forceinline__ void cp16(uint32_t to, const void *from) {
+    if (L1)
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+    else
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+}
+__device__ __forceinline__ uint4 lds16(uint32_t at) {
+    uint4 v;
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at) : "memory");
+    return v;
 }
 // 8 channels, as loaded.
 template <bool BF16>
 struct Raw;
 template <>
 struct Raw<true> {
+    static constexpr int CHUNKS = 1;                 // of 16 bytes
     uint4 v;
+    __device__ __forceinline__ void take(uint32_t at, int) { v = lds16(at); }
     __device__ __forceinline__ void load(const void *p, int64_t i) {
         v = *reinterpret_cast<const uint4 *>(reinterpret_cast<const __nv_bfloat16 *>(p) + i);
     }
@@ -183,7 +204,13 @@ struct Raw<true> {
 };
 template <>
 struct Raw<false> {
+    static constexpr int CHUNKS = 2;
     float4 u, v;
+    __device__ __forceinline__ void take(uint32_t at, int step) {
+        const uint4 x = lds16(at), y = lds16(at + step);
+        u = *reinterpret_cast<const float4 *>(&x);
+        v = *reinterpret_cast<const float4 *>(&y);
+    }
     __device__ __forceinline__ void load(const void *p, int64_t i) {
         const float4 *q = reinterpret_cast<const float4 *>(reinterpret_cast<const float *>(p) + i);
         u = q[0];
@@ -272,23 +299,38 @@ __device__ __forceinline__ uint32_t finite_top(const Raw<BF16> &r, bool &bad) {
 // THR threads (whole warps) share a head's tile of the page, all its tokens in
 // registers: the largest magnitude over them, then the codes; keys and values of a
 // head together. Each thread has the same TPT tasks of every head, so its angles
-// are computed once for the block's heads. Queries have no scale: they stream.
-// Bound by memory: each token is read once and written once. One pass with the
-// tile in registers reads half of what a pass for the scale and one for the codes
-// would. 24,213 bfloat16 tokens with 8 cache and 32 query heads of 128 (529 MB):
-// 117 us, 4.5 TB/s. What is left is the page's own turnaround: load, join the
-// maxima, round, store, with two to three blocks of 256 threads a multiprocessor to
-// cover it; three at TPT = 1 (80 registers) take 1,000 float32 tokens with 4 and 8
-// heads of 96 from 36.8 to 32.5 us, four 33.4, and one more register cut at TPT = 2
-// spills (117 to 122 us).
+// are computed once for the block's heads. Queries have no scale: they stream, a task
+// a thread. Bound by memory: each token is read once and written once. One pass with
+// the tile in registers reads half of what a pass for the scale and one for the codes
+// would; the next heads' tokens are on their way to shared memory meanwhile (registers
+// hold too few of them: 24,213 bfloat16 tokens with 8 cache and 32 query heads of 128,
+// 529 MB, 115 us so and 90 us with up to four heads' keys and values or eight heads'
+// queries under way, 5.9 TB/s; half as many heads under way 97 to 103). float32 and
+// side-by-side pairs read a 32-byte sector in two copies and go through L1 (2,051 tokens
+// of 4 sequences, 16 heads of 64: 27 us, past it 34).
+// A thread's copies of 16 bytes go to slots of its own, so that no barrier stands
+// between them and its reads: the copies of a stage are 256 threads of 16 bytes apart.
+template <bool BF16, int TPT>
+struct PageCfg {
+    static constexpr int BLOCKS = TPT == 1 ? (BF16 ? 3 : 2) : BF16 && TPT == 2 ? 2 : 1;      // a multiprocessor
+    static constexpr int ROOM = 196608 / BLOCKS;
+    static constexpr int CHUNKS = Raw<BF16>::CHUNKS, STEP = 256 * 16;
+    static constexpr int KV = 4 * TPT * CHUNKS * STEP, Q = 2 * CHUNKS * STEP;   // bytes of a stage
+    static constexpr int KV_STAGES = ROOM / KV < 4 ? ROOM / KV : 4, Q_STAGES = ROOM / Q < 8 ? ROOM / Q : 8;
+    static constexpr int BYTES = KV * KV_STAGES > Q * Q_STAGES ? KV * KV_STAGES : Q * Q_STAGES;
+    static_assert(KV_STAGES >= 1, "no room for a stage");
+};
 template <bool BF16, bool INTER, int TPT>
-__global__ void __launch_bounds__(256, TPT == 1 ? 3 : TPT == 2 ? 2 : 1) append_page_kernel(const AppendArgs a, const int thr, const int kv_parts,
-                                                          const int kv_heads, const int q_heads) {
+__global__ void __launch_bounds__(256, PageCfg<BF16, TPT>::BLOCKS)
+append_page_kernel(const AppendArgs a, const int thr, const int kv_parts, const int kv_heads, const int q_heads) {
+    using C = PageCfg<BF16, TPT>;
+    extern __shared__ __align__(16) uint8_t ring_sh[];
     __shared__ Slot sl;
     __shared__ uint64_t freq[64];
     __shared__ uint32_t red[2][8][2];
     __shared__ uint32_t bad_sh[8][4];                // by group: tokens with a channel that is not finite
     const int tid = threadIdx.x, D = a.c.D, page = a.c.page, H = a.c.H;
+    const uint32_t ring = (uint32_t)__cvta_generic_to_shared(ring_sh) + tid * 16;
     if (tid < a.rot / 2) freq[tid] = turns_of(a.inv_freq[tid]);
     find_slot(a, sl);
     if (sl.b < 0) return;
@@ -296,6 +338,50 @@ __global__ void __launch_bounds__(256, TPT == 1 ? 3 : TPT == 2 ? 2 : 1) append_p
     const int tasks = x.count * (D >> 4);
     const bool keys = (int)blockIdx.y < kv_parts;
     const int groups = 256 / thr, group = tid / thr, lane_in = tid - group * thr;
+    auto copy8 = [&](uint32_t to, const void *src, int64_t i) {
+        const uint8_t *from = static_cast<const uint8_t *>(src) + i * (BF16 ? 2 : 4);
+#pragma unroll
+        for (int y = 0; y < C::CHUNKS; ++y) cp16<!BF16 || INTER>(to + y * C::STEP, from + 16 * y);
+    };
+    if (!keys) {
+        // one task a thread, Q_STAGES heads of it on their way
+        const int part = ((int)blockIdx.y - kv_parts) / TPT, chunk = ((int)blockIdx.y - kv_parts) % TPT;
+        const int id = lane_in + chunk * thr;
+        if (group >= groups || id >= tasks) return;
+        Task k;
+        k.turned = false;
+        place_task<INTER>(a, id, k);
+        const int h0 = part * q_heads + group, h1 = imin(a.Hq, (part + 1) * q_heads);
+        const int64_t from = (x.t + k.t) * a.q_st, to = (x.t + k.t) * a.Hq * D;
+        auto fetch = [&](int h, int i) {
+            if (h < h1) {
+                const uint32_t at = ring + i % C::Q_STAGES * C::Q;
+                copy8(at, a.Q, from + (int64_t)h * D + k.a);
+                copy8(at + C::CHUNKS * C::STEP, a.Q, from + (int64_t)h * D + k.b);
+            }
+            asm volatile("cp.async.commit_group;" ::: "memory");
+        };
+#pragma unroll 1
+        for (int i = 0; i < C::Q_STAGES; ++i) fetch(h0 + i * groups, i);
+        turn_task(x, k, freq);
+#pragma unroll 1
+        for (int h = h0, i = 0; h < h1; h += groups, ++i) {
+            asm volatile("cp.async.wait_group %0;" ::"n"(C::Q_STAGES - 1) : "memory");
+            const uint32_t at = ring + i % C::Q_STAGES * C::Q;
+            Raw<BF16> r[2];
+            r[0].take(at, C::STEP);
+            r[1].take(at + C::CHUNKS * C::STEP, C::STEP);
+            float u[8], v[8];
+            r[0].get(u);
+            r[1].get(v);
+            rotate<INTER>(k, u, v);
+            fetch(h + C::Q_STAGES * groups, i);
+            Raw<BF16>::store(a.Q_out, to + (int64_t)h * D + k.a, u);
+            Raw<BF16>::store(a.Q_out, to + (int64_t)h * D + k.b, v);
+        }
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        return;
+    }
     Task k[TPT];
     bool on[TPT];
 #pragma unroll
@@ -303,55 +389,50 @@ __global__ void __launch_bounds__(256, TPT == 1 ? 3 : TPT == 2 ? 2 : 1) append_p
         const int id = lane_in + i * thr;
         on[i] = group < groups && id < tasks;
         k[i].turned = false;
-        if (on[i]) make_task<INTER>(a, x, id, k[i], freq);
-    }
-    if (!keys) {
-        const int h0 = ((int)blockIdx.y - kv_parts) * q_heads, h1 = imin(a.Hq, h0 + q_heads);
-        for (int h = h0 + group; h < h1; h += groups) {
-            Raw<BF16> r[TPT][2];
-#pragma unroll
-            for (int i = 0; i < TPT; ++i)
-                if (on[i]) {
-                    const int64_t row = (x.t + k[i].t) * a.q_st + (int64_t)h * D;
-                    r[i][0].load(a.Q, row + k[i].a);
-                    r[i][1].load(a.Q, row + k[i].b);
-                }
-#pragma unroll
-            for (int i = 0; i < TPT; ++i)
-                if (on[i]) {
-                    float u[8], v[8];
-                    r[i][0].get(u);
-                    r[i][1].get(v);
-                    rotate<INTER>(k[i], u, v);
-                    const int64_t o = ((x.t + k[i].t) * a.Hq + h) * D;
-                    Raw<BF16>::store(a.Q_out, o + k[i].a, u);
-                    Raw<BF16>::store(a.Q_out, o + k[i].b, v);
-                }
-        }
-        return;
+        if (on[i]) place_task<INTER>(a, id, k[i]);
     }
     const int h0 = (int)blockIdx.y * kv_heads, h1 = imin(H, h0 + kv_heads);
-    int parity = 0;
-    for (int base = h0; base < h1; base += groups, parity ^= 1) {
-        const int h = base + group;
+    auto fetch = [&](int h, int n) {
+        if (h < h1) {
+#pragma unroll
+            for (int kv = 0; kv < 2; ++kv)
+#pragma unroll
+                for (int i = 0; i < TPT; ++i)
+                    if (on[i]) {
+                        const uint32_t at = ring + n % C::KV_STAGES * C::KV + (kv * TPT + i) * 2 * C::CHUNKS * C::STEP;
+                        const int64_t row = (x.t + k[i].t) * (kv ? a.v_st : a.k_st) + (int64_t)h * D;
+                        copy8(at, kv ? a.V : a.K, row + k[i].a);
+                        copy8(at + C::CHUNKS * C::STEP, kv ? a.V : a.K, row + k[i].b);
+                    }
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+#pragma unroll 1
+    for (int n = 0; n < C::KV_STAGES; ++n) fetch(h0 + group + n * groups, n);
+#pragma unroll
+    for (int i = 0; i < TPT; ++i)
+        if (on[i]) turn_task(x, k[i], freq);
+    int n = 0;
+#pragma unroll 1
+    for (int base = h0; base < h1; base += groups, ++n) {
+        const int h = base + group, parity = n & 1;
         const bool live = group < groups && h < h1;
         const int64_t ph = (int64_t)x.page * H + h;
         Raw<BF16> r[2][TPT][2];
         int was[2] = {kEMin, kEMin};
         uint32_t top[2] = {0, 0};
+        asm volatile("cp.async.wait_group %0;" ::"n"(C::KV_STAGES - 1) : "memory");
         if (live) {
 #pragma unroll
             for (int kv = 0; kv < 2; ++kv) {
-                const void *src = kv ? a.V : a.K;
-                const int64_t st = kv ? a.v_st : a.k_st;
 #pragma unroll
                 for (int i = 0; i < TPT; ++i) {
                     r[kv][i][0].zero();
                     r[kv][i][1].zero();
                     if (on[i]) {
-                        const int64_t row = (x.t + k[i].t) * st + (int64_t)h * D;
-                        r[kv][i][0].load(src, row + k[i].a);
-                        r[kv][i][1].load(src, row + k[i].b);
+                        const uint32_t at = ring + n % C::KV_STAGES * C::KV + (kv * TPT + i) * 2 * C::CHUNKS * C::STEP;
+                        r[kv][i][0].take(at, C::STEP);
+                        r[kv][i][1].take(at + C::CHUNKS * C::STEP, C::STEP);
                     }
                 }
                 if (x.off) was[kv] = exponent_in((kv ? a.c.vs : a.c.ks)[ph]);
@@ -361,6 +442,7 @@ __global__ void __launch_bounds__(256, TPT == 1 ? 3 : TPT == 2 ? 2 : 1) append_p
 #pragma unroll
                 for (int i = 0; i < TPT; ++i) top[kv] = max(top[kv], max(r[kv][i][0].top(), r[kv][i][1].top()));
         }
+        fetch(h + C::KV_STAGES * groups, n);
         auto reduce = [&]() {
 #pragma unroll
             for (int kv = 0; kv < 2; ++kv) {
@@ -588,19 +670,32 @@ __global__ void __launch_bounds__(256) append_kernel(const AppendArgs a) {
 }
 
 template <bool BF16, bool INTER>
-void launch_pages(const AppendArgs &a, unsigned slots, int thr, int tpt, cudaStream_t st) {
-    // as many heads a block as leave a few blocks a multiprocessor: the angles are per block
-    const int groups = 256 / thr;
-    int kv = 8, q = 16;
-    while (kv > groups && (int64_t)slots * ((a.c.H + kv - 1) / kv + (a.Hq + q - 1) / q) < 1200) {
+cudaError_t launch_pages(const AppendArgs &a, unsigned slots, int thr, int tpt, cudaStream_t st) {
+    // as many heads a block as leave every multiprocessor its blocks: angles are computed and
+    // the first loads waited for once a block
+    const int groups = 256 / thr, chunks = tpt > 2 ? 4 : tpt;
+    const int want = 152 * (chunks == 1 ? PageCfg<BF16, 1>::BLOCKS : chunks == 2 ? PageCfg<BF16, 2>::BLOCKS : PageCfg<BF16, 4>::BLOCKS);
+    int kv = 16, q = 32;
+    auto parts = [&](int heads, int each) { return (heads + each - 1) / each; };
+    while (kv > groups && (int64_t)slots * (parts(a.c.H, kv) + parts(a.Hq, q) * chunks) < want) {
         kv /= 2;
         q /= 2;
     }
-    const int kv_parts = (a.c.H + kv - 1) / kv, q_parts = a.Q ? (a.Hq + q - 1) / q : 0;
-    const dim3 grid(slots, kv_parts + q_parts);
-    if (tpt == 1) append_page_kernel<BF16, INTER, 1><<<grid, 256, 0, st>>>(a, thr, kv_parts, kv, q);
-    else if (tpt == 2) append_page_kernel<BF16, INTER, 2><<<grid, 256, 0, st>>>(a, thr, kv_parts, kv, q);
-    else append_page_kernel<BF16, INTER, 4><<<grid, 256, 0, st>>>(a, thr, kv_parts, kv, q);
+    // Without queries all blocks take as long, and a second round of few of them as long as
+    // one of all (8 sequences of 3,000 tokens, 16 heads of 128, pages of 128: 96 us with 1.26
+    // rounds, 81 with 2.5; from some 1.6 rounds on more blocks lose more than they gain).
+    if (a.Hq == 0 && kv > groups && 10 * (int64_t)slots * parts(a.c.H, kv) < 14 * want) kv /= 2;
+    const int kv_parts = parts(a.c.H, kv);
+    const dim3 grid(slots, kv_parts + parts(a.Hq, q) * chunks);
+    auto launch = [&](auto k, SharedMemoryLimit &limit, int bytes) {
+        const cudaError_t e = limit.raise((const void *)k, bytes);
+        if (e == cudaSuccess) k<<<grid, 256, bytes, st>>>(a, thr, kv_parts, kv, q);
+        return e;
+    };
+    static SharedMemoryLimit limits[3];
+    if (tpt == 1) return launch(append_page_kernel<BF16, INTER, 1>, limits[0], PageCfg<BF16, 1>::BYTES);
+    if (tpt == 2) return launch(append_page_kernel<BF16, INTER, 2>, limits[1], PageCfg<BF16, 2>::BYTES);
+    return launch(append_page_kernel<BF16, INTER, 4>, limits[2], PageCfg<BF16, 4>::BYTES);
 }
 
 }  // namespace
@@ -635,13 +730,15 @@ cudaError_t launch_append(const AppendArgs &args, bool bf16, cudaStream_t st) {
     } else {
         const int tasks = page * (a.c.D / 16), thr = tasks >= 256 ? 256 : (tasks + 31) / 32 * 32;
         const int tpt = (tasks + thr - 1) / thr, up = tpt > 2 ? 4 : tpt;
+        cudaError_t e;
         if (bf16) {
-            if (a.inter) launch_pages<true, true>(a, (unsigned)slots, thr, up, st);
-            else launch_pages<true, false>(a, (unsigned)slots, thr, up, st);
+            if (a.inter) e = launch_pages<true, true>(a, (unsigned)slots, thr, up, st);
+            else e = launch_pages<true, false>(a, (unsigned)slots, thr, up, st);
         } else {
-            if (a.inter) launch_pages<false, true>(a, (unsigned)slots, thr, up, st);
-            else launch_pages<false, false>(a, (unsigned)slots, thr, up, st);
+            if (a.inter) e = launch_pages<false, true>(a, (unsigned)slots, thr, up, st);
+            else e = launch_pages<false, false>(a, (unsigned)slots, thr, up, st);
         }
+        if (e != cudaSuccess) return e;
     }
     note_launch();
     return cudaGetLastError();
