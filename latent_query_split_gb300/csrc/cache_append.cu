@@ -716,9 +716,9 @@ cudaError_t launch_append(const AppendArgs &args, bool bf16, cudaStream_t st) {
         else
             append_kernel<false><<<grid, 256, 0, st>>>(a);
     } else if (a.c.B > 8 && a.T <= 8 * (int64_t)a.c.B) {
-        // (8 cache and 32 query heads of 128, us by warps and by pages: 1 sequence of 1 token 5.8
-        // and 4.8, 8 of 8 9.2 and 5.8, 16 of 1 5.9 and 7.6, 16 of 8 9.1 and 8.8, 32 of 1 6.0 and
-        // 10.8, of 8 9.4 and 14.5, of 16 14.6 and 14.8)
+        // (8 cache and 32 query heads of 128, us by warps and by pages: 1 sequence of 1 token 5.6
+        // and 4.8, 8 of 8 8.9 and 6.5, 12 of 1 6.1 and 7.3, 16 of 8 9.2 and 8.5, 32 of 1 6.0 and
+        // 8.3, of 8 9.0 and 12.8, of 16 14.9 and 13.0, 256 of 8 17 and 25, of 16 33 and 27)
         const dim3 grid((unsigned)slots, (a.c.H + (a.Hq + kQHeads - 1) / kQHeads + 7) / 8);
         if (bf16) {
             if (a.inter) append_token_kernel<true, true><<<grid, 256, 0, st>>>(a);
