@@ -118,7 +118,9 @@ flare_status_t attn_run(const flare_cache_dims_t *d, const flare_cache_t *cache,
     AttnArgs a;
     a.c = make_pool(d, cache);
     a.G = G;
-    a.sl2 = (d->scale > 0.f ? d->scale : 1.0f / std::sqrt((float)d->D)) * 1.4426950408889634f;
+    const double sl2 = (d->scale > 0.f ? (double)d->scale : 1.0 / std::sqrt((double)d->D)) * 1.4426950408889634;
+    a.sl2 = (float)sl2;
+    a.sl2_rest = a.sl2 > 0.f && a.sl2 < INFINITY ? (float)((sl2 - a.sl2) / a.sl2) : 0.f;
     a.lens = lens;
     a.cu = cu;
     a.n = cu ? 0 : (int)(T / d->B);

@@ -142,6 +142,7 @@ template <class C>
 struct State {
     float c[C::MT][2], m[C::MT][2], l[C::MT][2];          // factors of the rows, references, sums
     int lim[C::MT][2], min_lim;                           // tokens that the rows see
+    float rest;                                           // what the rounding of the score scale took off
     uint32_t q[C::QREG ? C::KS : 1][4];
     float o[C::MT][C::NO][4];
     __device__ __forceinline__ void clear() {
@@ -242,6 +243,15 @@ __device__ __forceinline__ void unit(State<C> &z, uint32_t st, uint32_t q_at, in
         for (int n = 0; n < 2; ++n)
 #pragma unroll
             for (int y = 0; y < 4; ++y) s[x][n][y] = 0.f;
+    // float32: the two parts apart and 64 channels at a time, since the tensor cores cut a sum
+    // off where they do not round it
+    float hi[MT][2][4], lo[MT][2][4];
+#pragma unroll
+    for (int x = 0; x < MT; ++x)
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+            for (int y = 0; y < 4; ++y) hi[x][n][y] = lo[x][n][y] = 0.f;
 #pragma unroll
     for (int j = 0; j < KJ; ++j) {
         const uint4 ka = lds16(st + j * 512 + lane * 16), kb = lds16(st + (KJ + j) * 512 + lane * 16);
@@ -262,10 +272,21 @@ __device__ __forceinline__ void unit(State<C> &z, uint32_t st, uint32_t q_at, in
                         const uint4 v = lds16(q_at + ((x * C::PARTS + part) * KS + j * 4 + q) * 512 + lane * 16);
                         f[0] = v.x; f[1] = v.y; f[2] = v.z; f[3] = v.w;
                     }
-                    mma16816(s[x][0], f, a0, a1);
-                    mma16816(s[x][1], f, b0, b1);
+                    float (&to)[2][4] = !F32 ? s[x] : part ? lo[x] : hi[x];
+                    mma16816(to[0], f, a0, a1);
+                    mma16816(to[1], f, b0, b1);
                 }
         }
+        if (F32)
+#pragma unroll
+            for (int x = 0; x < MT; ++x)
+#pragma unroll
+                for (int n = 0; n < 2; ++n)
+#pragma unroll
+                    for (int y = 0; y < 4; ++y) {
+                        s[x][n][y] += j + 1 < KJ ? hi[x][n][y] : hi[x][n][y] + lo[x][n][y];
+                        hi[x][n][y] = 0.f;
+                    }
     }
     const uint2 sc = lds8(st + C::UNIT - 256 + lane * 8);
     const float ks = __uint_as_float(sc.x), vs = __uint_as_float(sc.y);
@@ -286,12 +307,17 @@ __device__ __forceinline__ void unit(State<C> &z, uint32_t st, uint32_t q_at, in
                     const int n = n0 + 2 * t + (e & 1) + 8 * (e >> 1);
                     if (vs == 0.f || n >= lim[x][y] || n >= end) hidden |= 1u << e;
                 }
-            // exponents of the weights against reference `ref`: one rounding each
+            // Exponents of the weights against reference `ref`. float32: ref is a whole number, so
+            // that ev - ref is exact and what is rounded is small where the weight is large, and
+            // the rounding of the score scale is made up for (either would put scores of 40 off by
+            // 2e-6). bf16: ref is such that the largest weight met so far is a power of two, which
+            // fp16 holds without a rounding.
             float u[4];
             auto exponents = [&](float ref) {
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     u[e] = fmaf(v[e], cc, ev - ref);
+                    if (F32) u[e] = fmaf(v[e] * cc, z.rest, u[e]);
                     if (hidden >> e & 1) u[e] = -INFINITY;
                 }
                 return fmaxf(fmaxf(u[0], u[1]), fmaxf(u[2], u[3]));
@@ -301,8 +327,8 @@ __device__ __forceinline__ void unit(State<C> &z, uint32_t st, uint32_t q_at, in
                 best = fmaxf(best, __shfl_xor_sync(0xffffffffu, best, 1));
                 best = fmaxf(best, __shfl_xor_sync(0xffffffffu, best, 2));
                 if (best > m[x][y] + kHeadroom) {
-                    const float f = tc::ex2(m[x][y] - (best - kFresh));
-                    m[x][y] = best - kFresh;
+                    const float top = F32 ? rintf(best - kFresh) : best - kFresh, f = tc::ex2(m[x][y] - top);
+                    m[x][y] = top;
                     l[x][y] *= f;
 #pragma unroll
                     for (int j = 0; j < NO; ++j) {
@@ -349,8 +375,18 @@ __device__ __forceinline__ void unit(State<C> &z, uint32_t st, uint32_t q_at, in
         for (int j = 0; j < 4; ++j)
 #pragma unroll
             for (int x = 0; x < MT; ++x) {
-                if (F32) mma16816(o[x][4 * q + j], pr[x], b0[j], b1[j]);
-                mma16816(o[x][4 * q + j], pf[x], b0[j], b1[j]);
+                if (F32) {
+                    // The tensor cores cut a sum off where they do not round it: into o that would
+                    // take a bit off what a large weight left there with every unit that follows,
+                    // so the unit's share is added with a rounding.
+                    float v[4] = {0.f, 0.f, 0.f, 0.f};
+                    mma16816(v, pr[x], b0[j], b1[j]);
+                    mma16816(v, pf[x], b0[j], b1[j]);
+#pragma unroll
+                    for (int y = 0; y < 4; ++y) o[x][4 * q + j][y] += v[y];
+                } else {
+                    mma16816(o[x][4 * q + j], pf[x], b0[j], b1[j]);
+                }
             }
     }
 }
@@ -418,6 +454,7 @@ __device__ __forceinline__ void load_rows(const AttnArgs &a, const Cursor &cur, 
                                           int lane) {
     const int g = lane >> 2, t = lane & 3, D = a.c.D;
     z.min_lim = end;
+    z.rest = a.sl2_rest;
 #pragma unroll 1
     for (int rr = 0; rr < 2 * C::MT; ++rr) {
         float x[C::KJ][2][8];
@@ -591,7 +628,7 @@ __global__ void __launch_bounds__(C::NT, 2) attn_mma_span_kernel(const __grid_co
 // no workspace, for calls so small that a second launch would cost as much as the
 // attention. One token of 4 queries a head, 8 heads of 128, 1,500 tokens: 8.1 us; 3 tokens
 // of 5 queries, 6 sequences of 2 to 9,000, 4 heads of 64: 18.5 (the longest sequence's 563
-// units are 12 rounds of its 48 warps); float32, 500 to 7,000 tokens, 4 heads of 64: 14.5.
+// units are 12 rounds of its 48 warps); float32, 500 to 7,000 tokens, 4 heads of 64: 15.1.
 // The states of a block's warps become one: sink(r, d, M, l, v) gets channels d .. d + 3 of
 // row r, with reference M and sum l. `at`: shared memory (JOIN bytes) that the warps may
 // have used until now.

@@ -25,7 +25,7 @@ struct Pool {
 struct AttnArgs {
     Pool c;
     int G;                              // query heads of one cache head
-    float sl2;                          // score scale * log2(e)
+    float sl2, sl2_rest;                // score scale * log2(e); it is sl2 (1 + sl2_rest)
     const int32_t *lens, *cu;
     int n;                              // rows a sequence where cu is null
     int64_t T;
